@@ -288,6 +288,103 @@ int x1cb_pack_stem(const int8_t *nhwc, int8_t *folded, int B, int H, int W, int 
 int x1cb_pack_stem_weight(const int8_t *oihw, int8_t *blocked, int Oc, int Cin, int R,
                           void *stream);
 
+/*
+ * Floating-point operators.
+ *
+ * Tensors are channels last: [B, H, W, C], element (b, h, w, c) at
+ * ((b*H + h)*W + w)*C + c.  dtype is one of X1CB_F32, X1CB_BF16, X1CB_F16 and
+ * act one of X1CB_ACT_NONE (v), X1CB_ACT_RELU (max(v, 0); NaN stays NaN),
+ * X1CB_ACT_SILU (v / (1 + exp(-v))); other values return X1CB_ERR_SHAPE.
+ * Sums, statistics and everything between the load and the store are 32-bit;
+ * a result is rounded once, to nearest even.  Empty tensors are a no-op.
+ * The rules on memory, alignment, overlap, streams and errors above hold
+ * (gamma, beta and bias: 4-byte alignment).
+ *
+ * MX4: the OCP microscaling format MXFP4.  A [M, K] matrix (K a multiple of
+ * 32) is stored as two arrays:
+ *   codes  [M, K/2] bytes, two e2m1 codes per byte, element 2j in the low
+ *          half of byte j: code = sign << 3 | index into {0, 0.5, 1, 1.5, 2,
+ *          3, 4, 6};
+ *   scales one byte s per row and block of 32 elements, worth 2^(s - 127)
+ *          (255: NaN), in tiles of 128 rows x 4 blocks: row m, block b at byte
+ *          ((m/128)*ceil(K/128) + b/4)*512 + (m%32)*16 + (m%128)/32*4 + b%4,
+ *          x1cb_mx4_scale_size(M, K) bytes in all.  Scale bytes of blocks past
+ *          K must not be 255 (the calls that write scales write all padding 0).
+ * For activations M = B*H*W (row = pixel) and K = C.
+ */
+#define X1CB_F32 0
+#define X1CB_BF16 1
+#define X1CB_F16 2
+#define X1CB_ACT_NONE 0
+#define X1CB_ACT_RELU 1
+#define X1CB_ACT_SILU 2
+
+/* Bytes of device workspace the group_norm_act calls need (0 where an image's
+ * statistics stay on chip); workspace may be NULL then. */
+size_t group_norm_workspace_size(int dtype, int B, int H, int W, int C, int G);
+
+/*
+ * Group norm with an optional shortcut Sum and an activation, the counterpart
+ * of folded BN + Sum + ReLU for a norm that depends on its input: with mu and
+ * var the mean and the (biased) variance of image b over the H*W*(C/G) values
+ * of c's group,
+ *   y = act((x - mu) / sqrt(var + eps) * gamma[c] + beta[c] + r)
+ *   x, r, y [B, H, W, C] of `dtype` (r may be NULL); gamma, beta [C] float
+ *   (NULL: 1, 0); G groups, C % G == 0; C <= 8192; eps >= 0.
+ */
+int group_norm_act(const void *x, int dtype, const float *gamma, const float *beta,
+                   const void *r, int act, float eps, void *y, void *workspace,
+                   size_t ws_bytes, int B, int H, int W, int C, int G, void *stream);
+
+/* The same, quantised for the int8 convolutions:
+ *   q = min(max(rint(y * q_mul), -128), 127) (NaN: 0), C % 32 == 0;
+ *   q [B, C/32, H, W, 32] int8, the NC/32HW32 layout they read. */
+int group_norm_act_i8(const void *x, int dtype, const float *gamma, const float *beta,
+                      const void *r, int act, float eps, float q_mul, int8_t *q,
+                      void *workspace, size_t ws_bytes, int B, int H, int W, int C, int G,
+                      void *stream);
+
+/* The same, quantised to MX4 (as x1cb_quantize_mx4 of the unrounded y) for
+ * conv1x1_bias_add_act_mx4, C % 32 == 0:
+ *   q [B*H*W, C/2] codes, sf scales. */
+int group_norm_act_mx4(const void *x, int dtype, const float *gamma, const float *beta,
+                       const void *r, int act, float eps, uint8_t *q, uint8_t *sf,
+                       void *workspace, size_t ws_bytes, int B, int H, int W, int C, int G,
+                       void *stream);
+
+/* Bytes of the scales of an [M, K] MX4 matrix: ceil(M/128)*ceil(K/128)*512
+ * (0 for a negative size). */
+size_t x1cb_mx4_scale_size(long long M, int K);
+
+/*
+ * x [M, K] of `dtype` -> MX4.  Per block: s = clamp(floor(log2 max|x|) - 2 +
+ * 127, 0, 254) (0 for a block of zeros); code = x * 2^(127 - s) rounded to the
+ * nearest e2m1 value, ties to the even code, at most +-6.  A block that holds
+ * an infinity or a NaN gets s = 255 and zero codes: its 32 values read back as
+ * NaN.  K % 32 == 0, M <= 2^31 - 1.
+ */
+int x1cb_quantize_mx4(const void *x, int dtype, uint8_t *q, uint8_t *sf, long long M, int K,
+                      void *stream);
+
+/* MX4 -> the values it stands for, x [M, K] of `dtype`. */
+int x1cb_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtype, long long M,
+                        int K, void *stream);
+
+/*
+ * Fused 1x1 convolution of MX4 operands + bias + shortcut Sum + activation:
+ * the 4-bit form of conv1x1_bn_add_relu_i8 with a floating-point epilogue, and
+ * with H = W = 1 a fully connected layer.
+ *   out[m, o] = act(sum_k x[m, k] * w[o, k] + bias[o] + r[m, o]),  m = (b, h, w)
+ *   x [B*H*W, Ic/2], xs  MX4 activations (read); w [Oc, Ic/2], ws MX4 weights
+ *   (read); bias [Oc] float or NULL; r [B, H, W, Oc] of `dtype` or NULL;
+ *   out [B, H, W, Oc] of `dtype` (written).
+ * Ic % 32 == 0, Ic <= 65536; 1 <= Oc <= 65536; B*H*W <= 2^31 - 1.
+ */
+int conv1x1_bias_add_act_mx4(const uint8_t *x, const uint8_t *xs, const uint8_t *w,
+                             const uint8_t *ws, const float *bias, const void *r, int act,
+                             void *out, int dtype, int B, int H, int W, int Ic, int Oc,
+                             void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *x1cb_status_string(int status);
 

@@ -1,0 +1,323 @@
+"""MX4 conversions and the MX4 1x1 convolution against the 64-bit definition,
+and the operators as they run together."""
+import pytest
+import torch
+
+import x1_conv_bn_b200 as X
+from oracle import float_ref as F
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+IDS = ["f32", "bf16", "f16"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from x1_conv_bn_b200 import _build
+
+    _build.build()
+    X.lib()
+    X.x1cb_debug_inject(0)
+    X.x1cb_set_wait_limit_ns(0)
+    X.x1cb_last_device_error(clear=True)
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _clean():
+    torch.cuda.synchronize()
+    st, bits = X.x1cb_last_device_error(clear=True)
+    assert st == 0, bits
+
+
+MK = [(1, 32), (1, 2048), (3, 96), (127, 128), (128, 160), (129, 64), (1000, 544), (5, 4096),
+      (4096, 32), (2, 65536)]
+
+
+@pytest.mark.parametrize("M,K", MK)
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_quantize(M, K, dtype):
+    g = _gen(M + K)
+    x = torch.randn(M, K, generator=g, device=DEV)
+    x = x * torch.exp(2 * torch.randn(M, K // 32, generator=g, device=DEV)).repeat_interleave(32, 1)
+    x[:, ::7] = 0
+    x = x.to(dtype)
+    x[0, :32] = 0  # a block of zeros
+    q, sf = X.x1cb_quantize_mx4(x)
+    codes, s = F.quantize_mx4(x)
+    wq, wsf = F.pack_mx4(codes, s)
+    assert torch.equal(sf, wsf)
+    assert torch.equal(q, wq)
+    v = F.values_mx4(codes, s)
+    for dt in DTYPES:
+        got = X.x1cb_dequantize_mx4(q, sf, dtype=dt)
+        assert got.dtype == dt and torch.equal(got, v.to(dt))
+
+
+def test_quantize_ties_and_borders():
+    """Every midpoint of the e2m1 grid and its neighbours, at many scales, each
+    beside the block's largest value."""
+    mid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.99], device=DEV)
+    up = torch.nextafter(mid, torch.full_like(mid, 9.0))
+    dn = torch.nextafter(mid, torch.zeros_like(mid))
+    row = torch.cat((mid, up, dn, torch.tensor([7.5, 4.0], device=DEV)))
+    e = torch.tensor([-140, -130, -128, -127, -126, -100, -1, 0, 1, 50, 124, 125], device=DEV)
+    x = torch.cat([row * (2.0 ** int(k)) if k > -120 else (row.double() * 2.0 ** int(k)).float()
+                   for k in e.tolist()]).view(len(e), 32)
+    x = torch.cat((x, -x))
+    q, sf = X.x1cb_quantize_mx4(x)
+    wq, wsf = F.pack_mx4(*F.quantize_mx4(x))
+    assert torch.equal(sf, wsf) and torch.equal(q, wq)
+
+
+def test_quantize_not_finite():
+    x = torch.randn(4, 96, generator=_gen(1), device=DEV)
+    x[1, 40] = float("inf")
+    x[2, 0] = float("nan")
+    x[3, 95] = -float("inf")
+    q, sf = X.x1cb_quantize_mx4(x)
+    wq, wsf = F.pack_mx4(*F.quantize_mx4(x))
+    assert torch.equal(sf, wsf) and torch.equal(q, wq)
+    v = X.x1cb_dequantize_mx4(q, sf, dtype=torch.float32)
+    bad = torch.zeros(4, 96, dtype=torch.bool, device=DEV)
+    bad[1, 32:64] = bad[2, :32] = bad[3, 64:] = True
+    assert torch.equal(torch.isnan(v), bad)
+
+
+def test_dequantize_every_code_and_scale():
+    codes = torch.arange(16, device=DEV).repeat(256, 2)
+    s = torch.arange(256, device=DEV).view(256, 1)
+    q, sf = F.pack_mx4(codes, s)
+    v = F.values_mx4(codes, s)
+    for dt in DTYPES:
+        got, want = X.x1cb_dequantize_mx4(q, sf, dtype=dt), v.to(dt)
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        ok = ~torch.isnan(want)
+        assert torch.equal(got[ok], want[ok])
+
+
+def test_conversions_leave_the_rest_alone():
+    """Rows behind the last one are left as they were."""
+    x = torch.randn(5, 64, generator=_gen(2), device=DEV)
+    buf = torch.full((9, 32), 0xAB, dtype=torch.uint8, device=DEV)
+    sf = torch.empty(X.mx4_scale_shape(5, 64), dtype=torch.uint8, device=DEV)
+    X.x1cb_quantize_mx4(x, out=(buf[:5], sf))
+    assert (buf[5:] == 0xAB).all()
+    out = torch.full((9, 64), 7.0, device=DEV)
+    X.x1cb_dequantize_mx4(buf[:5], sf, dtype=torch.float32, out=out[:5])
+    assert (out[5:] == 7.0).all()
+
+
+# ---- the product ---------------------------------------------------------------
+
+def _operand(rows, K, g, spread=0.4):
+    x = torch.randn(rows, K, generator=g, device=DEV)
+    x = x * torch.exp(spread * torch.randn(rows, K // 32, generator=g, device=DEV)).repeat_interleave(32, 1)
+    codes, s = F.quantize_mx4(x)
+    return F.pack_mx4(codes, s), F.values_mx4(codes, s)
+
+
+def _conv(shape, dtype, act, bias, res, seed):
+    B, H, W, Ic, Oc = shape
+    g, M = _gen(seed), B * H * W
+    (x, xs), xv = _operand(M, Ic, g)
+    (w, ws), wv = _operand(Oc, Ic, g)
+    b = torch.randn(Oc, generator=g, device=DEV) if bias else None
+    r = torch.randn(B, H, W, Oc, generator=g, device=DEV).to(dtype) if res else None
+    y, size = F.conv1x1(xv, wv, b, r, act)
+    got = X.conv1x1_bias_add_act_mx4(x.view(B, H, W, Ic // 2), xs, w, ws, b, r, act=act,
+                                     dtype=dtype)
+    _clean()
+    assert got.shape == (B, H, W, Oc) and got.dtype == dtype
+    tol = F.conv_tolerance(y, size, Ic, dtype)
+    err = (got.double().view(M, Oc) - y).abs()
+    worst = (err - tol).max()
+    assert not torch.isnan(got).any() and worst <= 0, (float(worst), float(err.max()))
+
+
+CONV = [  # B, H, W, Ic, Oc
+    (1, 1, 1, 32, 1),        # one value
+    (1, 1, 1, 2048, 1000),   # a classifier head
+    (2, 1, 1, 96, 7),
+    (3, 1, 1, 4096, 130),
+    (1, 3, 5, 64, 128),
+    (1, 4, 4, 1024, 256),    # 16 rows
+    (1, 5, 5, 288, 260),     # 25 rows
+    (2, 6, 5, 512, 512),     # 60 rows
+    (2, 7, 9, 160, 66),      # a K tail of 32, odd channel tail
+    (1, 8, 16, 128, 64),     # one whole tile of rows
+    (3, 13, 11, 224, 200),
+    (7, 27, 29, 544, 200),
+    (5, 28, 28, 128, 512),
+    (2, 56, 56, 64, 256),
+    (1, 17, 19, 2080, 333),
+    (9, 16, 16, 1024, 1024),
+    (40, 16, 16, 256, 392),
+    (16, 32, 32, 512, 2048),
+    (1, 129, 127, 32, 8),
+]
+
+
+@pytest.mark.parametrize("shape", CONV, ids=[str(s) for s in CONV])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("act,bias,res", [("none", False, False), ("relu", True, True),
+                                          ("silu", True, False)])
+def test_conv(shape, dtype, act, bias, res):
+    _conv(shape, dtype, act, bias, res, sum(shape))
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 4096, 256), (1, 7, 7, 4096, 512), (3, 16, 16, 4096, 384),
+                                   (9, 16, 16, 608, 1000)])
+def test_conv_exact(shape):
+    """Operands whose sums fit 24 bits whatever their order: the result has to
+    be exact, so that one wrong scale or element shows."""
+    B, H, W, Ic, Oc = shape
+    g, M = _gen(sum(shape)), B * H * W
+    pair = []
+    for rows in (M, Oc):
+        codes = torch.randint(0, 16, (rows, Ic), generator=g, device=DEV)
+        s = torch.randint(126, 129, (rows, Ic // 32), generator=g, device=DEV)
+        pair.append((F.pack_mx4(codes, s), F.values_mx4(codes, s)))
+    (x, xs), xv = pair[0]
+    (w, ws), wv = pair[1]
+    # terms are multiples of 1/16 and at most 6*2*6*2 = 144: 4096 of them stay below 2^20
+    got = X.conv1x1_bias_add_act_mx4(x.view(B, H, W, Ic // 2), xs, w, ws, act="none",
+                                     dtype=torch.float32)
+    _clean()
+    assert torch.equal(got.view(M, Oc).double(), xv @ wv.T)
+
+
+def test_conv_row_masks():
+    """Zero rows, and blocks whose scale is NaN: their row (or channel) alone is NaN."""
+    g = _gen(5)
+    (x, xs), xv = _operand(300, 256, g)
+    (w, ws), wv = _operand(140, 256, g)
+    x[17] = 0
+    codes, s = F.unpack_mx4(x, xs)
+    s[200, 3] = 255
+    x, xs = F.pack_mx4(codes, s)
+    wc, wsb = F.unpack_mx4(w, ws)
+    wsb[131, 0] = 255
+    w, ws = F.pack_mx4(wc, wsb)
+    got = X.conv1x1_bias_add_act_mx4(x.view(1, 300, 1, 128), xs, w, ws, act="none",
+                                     dtype=torch.float32).view(300, 140)
+    _clean()
+    bad = torch.zeros(300, 140, dtype=torch.bool, device=DEV)
+    bad[200] = True
+    bad[:, 131] = True
+    assert torch.equal(torch.isnan(got), bad)
+    assert (got[17][~bad[17]] == 0).all()
+
+
+@pytest.mark.parametrize("M,Oc", [(1, 100), (50, 136), (300, 200), (300, 7)])
+def test_conv_leaves_the_rest_alone(M, Oc):
+    g = _gen(6)
+    (x, xs), _ = _operand(M, 128, g)
+    (w, ws), _ = _operand(Oc, 128, g)
+    buf = torch.full((M + 140, Oc), 7.0, dtype=torch.bfloat16, device=DEV)
+    X.conv1x1_bias_add_act_mx4(x.view(1, M, 1, 64), xs, w, ws, out=buf[:M].view(1, M, 1, Oc))
+    _clean()
+    assert (buf[M:] == 7.0).all()
+
+
+def test_conv_empty_and_refused():
+    w, ws = X.x1cb_quantize_mx4(torch.ones(64, 128, device=DEV))
+    x = torch.empty((0, 4, 4, 64), dtype=torch.uint8, device=DEV)
+    xs = torch.empty((0, 1, 32, 16), dtype=torch.uint8, device=DEV)
+    assert X.conv1x1_bias_add_act_mx4(x, xs, w, ws).shape == (0, 4, 4, 64)
+    x, xs = X.x1cb_quantize_mx4(torch.ones(1, 4, 4, 128, device=DEV))
+    for call in (lambda: X.conv1x1_bias_add_act_mx4(x, xs, w[:, :32].contiguous(), ws),
+                 lambda: X.conv1x1_bias_add_act_mx4(x, xs[:, :, :, :8], w, ws),
+                 lambda: X.conv1x1_bias_add_act_mx4(x, xs, w, ws, dtype=torch.float64),
+                 lambda: X.conv1x1_bias_add_act_mx4(x, xs, w, ws, act="gelu"),
+                 lambda: X.conv1x1_bias_add_act_mx4(x, xs, w, ws, r=torch.zeros(1, 4, 4, 64, device=DEV)),
+                 lambda: X.conv1x1_bias_add_act_mx4(x, xs, w.cpu(), ws)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(X.X1cbError):
+        X.x1cb_quantize_mx4(torch.ones(4, 48, device=DEV))
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 2048, 1000), (1, 6, 6, 1024, 512),
+                                   (3, 28, 28, 256, 384)])
+def test_conv_capture_and_streams(shape):
+    B, H, W, Ic, Oc = shape
+    g, M = _gen(12), B * H * W
+    (x, xs), _ = _operand(M, Ic, g)
+    (x2, xs2), _ = _operand(M, Ic, g)
+    (w, ws), _ = _operand(Oc, Ic, g)
+    view = lambda t: t.view(B, H, W, Ic // 2)  # noqa: E731
+    want = X.conv1x1_bias_add_act_mx4(view(x), xs, w, ws)
+    want2 = X.conv1x1_bias_add_act_mx4(view(x2), xs2, w, ws)
+    bx, bs, out = x.clone(), xs.clone(), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        X.conv1x1_bias_add_act_mx4(view(bx), bs, w, ws, out=out)
+    for a, s, ref in ((x2, xs2, want2), (x, xs, want)):
+        bx.copy_(a)
+        bs.copy_(s)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = X.conv1x1_bias_add_act_mx4(view(x), xs, w, ws, stream=one)
+    b = X.conv1x1_bias_add_act_mx4(view(x2), xs2, w, ws, stream=two)
+    _clean()
+    assert torch.equal(a, want) and torch.equal(b, want2)
+
+
+# ---- together --------------------------------------------------------------------
+
+@pytest.mark.parametrize("shape", [(2, 14, 14, 256, 32, 64), (1, 1, 1, 2048, 32, 1000),
+                                   (3, 9, 7, 96, 3, 200)])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_norm_then_conv_then_norm(shape, dtype):
+    """A pre-activation block: norm + SiLU to MX4, the 1x1 product with a
+    shortcut, and a norm of the result; each step against the definition on the
+    library's own input to it, so that no rounding is counted twice."""
+    B, H, W, C, G, Oc = shape
+    g, M = _gen(sum(shape)), B * H * W
+    x = (2 * torch.randn(B, H, W, C, generator=g, device=DEV) + 1).to(dtype)
+    gamma = 1 + 0.1 * torch.randn(C, generator=g, device=DEV)
+    beta = 0.1 * torch.randn(C, generator=g, device=DEV)
+    w, ws = X.x1cb_quantize_mx4(torch.randn(Oc, C, generator=g, device=DEV) * C ** -0.5)
+    bias = torch.randn(Oc, generator=g, device=DEV)
+    r = torch.randn(B, H, W, Oc, generator=g, device=DEV).to(dtype)
+    q, sf = X.group_norm_act_mx4(x, gamma, beta, G, act="silu")
+    out = X.conv1x1_bias_add_act_mx4(q, sf, w, ws, bias, r, act="none", dtype=dtype)
+    xv = F.values_mx4(*F.unpack_mx4(q.view(M, C // 2), sf))
+    wv = F.values_mx4(*F.unpack_mx4(w, ws))
+    y, size = F.conv1x1(xv, wv, bias, r, "none")
+    assert ((out.double().view(M, Oc) - y).abs() <= F.conv_tolerance(y, size, C, dtype)).all()
+    # MX4 keeps two to three bits: the values are those of the norm to within a quarter
+    ref, _ = F.group_norm(x, gamma, beta, G, 1e-5, None, "silu")
+    top = ref.view(M, -1, 32).abs().amax(-1, keepdim=True).expand(-1, -1, 32).reshape(M, C)
+    assert ((xv - ref.view(M, C)).abs() <= 0.25 * top + 1e-6).all()
+    last = X.group_norm_act(out, None, None, 1, act="relu")
+    y2, size2 = F.group_norm(out, None, None, 1, 1e-5, None, "relu")
+    assert ((last.double() - y2).abs() <= F.norm_tolerance(y2, size2, dtype)).all()
+
+
+def test_norm_feeds_the_int8_convolution(oracle):
+    """group_norm_act_i8's output is what conv3x3_bn_relu_i8 reads: the chain
+    equals the oracle's convolution of the same int8 image, bit for bit."""
+    from x1_conv_bn_b200 import synth
+
+    s = synth.ConvShape(2, 14, 14, 128, 128, 3, False)
+    inp = synth.conv_inputs(s, 31)
+    x = torch.randn(2, 14, 14, 128, generator=_gen(31), device=DEV).bfloat16()
+    q = X.group_norm_act_i8(x, None, None, 32, 32.0)
+    got = X.conv3x3_bn_relu_i8(q, X.x1cb_pack_weight(inp.w.to(DEV)), inp.bias.to(DEV),
+                               inp.m.to(DEV), inp.S)
+    _clean()
+    img = X.x1cb_unpack_act(q).cpu()
+    ref = oracle.pack_act(oracle.conv(img, inp.w, inp.bias, inp.m, inp.S, None, 0))
+    assert torch.equal(got.cpu(), ref)

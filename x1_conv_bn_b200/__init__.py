@@ -82,6 +82,17 @@ def lib() -> ctypes.CDLL:
         L.stem_conv_bn_relu_maxpool_i8.argtypes = [vp] * 4 + [i32, vp] + [i] * 4 + [vp]
         L.x1cb_pack_stem.argtypes = [vp, vp] + [i] * 5 + [vp]
         L.x1cb_pack_stem_weight.argtypes = [vp, vp] + [i] * 3 + [vp]
+        f, ll = ctypes.c_float, ctypes.c_longlong
+        L.group_norm_workspace_size.argtypes = [i] * 6
+        L.group_norm_workspace_size.restype = sz
+        L.group_norm_act.argtypes = [vp, i, vp, vp, vp, i, f, vp, vp, sz] + [i] * 5 + [vp]
+        L.group_norm_act_i8.argtypes = [vp, i, vp, vp, vp, i, f, f, vp, vp, sz] + [i] * 5 + [vp]
+        L.group_norm_act_mx4.argtypes = [vp, i, vp, vp, vp, i, f, vp, vp, vp, sz] + [i] * 5 + [vp]
+        L.x1cb_mx4_scale_size.argtypes = [ll, i]
+        L.x1cb_mx4_scale_size.restype = sz
+        L.x1cb_quantize_mx4.argtypes = [vp, i, vp, vp, ll, i, vp]
+        L.x1cb_dequantize_mx4.argtypes = [vp, vp, vp, i, ll, i, vp]
+        L.conv1x1_bias_add_act_mx4.argtypes = [vp] * 6 + [i, vp, i] + [i] * 5 + [vp]
         _lib = L
     return _lib
 
@@ -422,6 +433,217 @@ def x1cb_pack_weight(oihw, out=None, stream=None):
                                     _dev(out, torch.int8, "out"), Oc, Ic, R,
                                     _stream(stream, oihw.device))
     _check(st, "x1cb_pack_weight")
+    return out
+
+
+# ---- floating-point operators ------------------------------------------------
+
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ACTS = {"none": 0, "relu": 1, "silu": 2}
+
+
+def _dtype(t: torch.dtype, name: str) -> int:
+    if t not in DTYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t}")
+    return DTYPES[t]
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _sized(t: Optional[torch.Tensor], shape, name: str):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _alloc_on(stream, device):
+    """Context in which outputs and workspaces are allocated: the stream the
+    call runs on, so that the allocator never hands out memory that work on
+    another stream still uses, or takes back a workspace too early."""
+    if stream is None:
+        return torch.cuda.stream(None)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if raw == 0:  # the legacy default stream
+            stream = torch.cuda.default_stream(device)
+        else:
+            stream = torch.cuda.ExternalStream(raw, device=device)
+    return torch.cuda.stream(stream)
+
+
+def group_norm_workspace_size(dtype, B: int, H: int, W: int, C: int, G: int) -> int:
+    """Bytes of workspace the group_norm_act calls need (dtype: of x)."""
+    return int(lib().group_norm_workspace_size(_dtype(dtype, "dtype"), B, H, W, C, G))
+
+
+def _norm(what, x, gamma, beta, G, eps, r, act, outs, workspace, stream, q_mul=None):
+    """Shared by the group_norm_act calls; outs(B, H, W, C, device) allocates or
+    checks the outputs."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError("x must be [B, H, W, C]")
+    B, H, W, C = x.shape
+    dt, a = _dtype(x.dtype, "x"), _act(act)
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        _sized(t, (C,), name)
+    _sized(r, x.shape, "r")
+    need = group_norm_workspace_size(x.dtype, B, H, W, C, int(G))
+    with _same_device(x, gamma, beta, r, workspace):
+        st = _stream(stream, x.device)
+        with _alloc_on(stream, x.device):
+            ys = outs(B, H, W, C, x.device)
+            if workspace is None and need:
+                workspace = torch.empty(need, dtype=torch.int8, device=x.device)
+        _same_device(x, *ys)
+        status = getattr(lib(), what)(
+            _dev(x, x.dtype, "x"), dt, _dev(gamma, torch.float32, "gamma"),
+            _dev(beta, torch.float32, "beta"), _dev(r, x.dtype, "r"), a, float(eps),
+            *([] if q_mul is None else [float(q_mul)]), *[_dev(y, y.dtype, "out") for y in ys],
+            _dev(workspace, torch.int8, "workspace"),
+            0 if workspace is None else workspace.numel(), B, H, W, C, int(G), st)
+    _check(status, what)
+    return ys
+
+
+def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str = "relu",
+                   out=None, workspace=None, stream=None):
+    """Group norm (+ shortcut Sum when r is given) + activation, channels last.
+
+    x, r, out [B, H, W, C] float32, bfloat16 or float16; gamma, beta [C]
+    float32 or None; G groups; act "none", "relu" or "silu"."""
+    def outs(B, H, W, C, device):
+        if out is None:
+            return [torch.empty((B, H, W, C), dtype=x.dtype, device=device)]
+        if out.dtype != x.dtype:
+            raise ValueError(f"out must be {x.dtype}, got {out.dtype}")
+        return [_sized(out, x.shape, "out")]
+
+    return _norm("group_norm_act", x, gamma, beta, G, eps, r, act, outs, workspace, stream)[0]
+
+
+def group_norm_act_i8(x, gamma, beta, G: int, q_mul: float, eps: float = 1e-5, r=None,
+                      act: str = "relu", out=None, workspace=None, stream=None):
+    """group_norm_act quantised for the int8 convolutions: clamp(rint(y * q_mul),
+    -128, 127) as NC/32HW32 [B, C/32, H, W, 32]."""
+    def outs(B, H, W, C, device):
+        shape = (B, C // 32, H, W, 32)
+        if out is None:
+            return [torch.empty(shape, dtype=torch.int8, device=device)]
+        if out.dtype != torch.int8:
+            raise ValueError(f"out must be int8, got {out.dtype}")
+        return [_sized(out, shape, "out")]
+
+    return _norm("group_norm_act_i8", x, gamma, beta, G, eps, r, act, outs, workspace, stream,
+                 q_mul)[0]
+
+
+def mx4_scale_shape(M: int, K: int):
+    """Shape of the scales of an [M, K] MX4 matrix: [ceil(M/128), ceil(K/128), 32, 16]."""
+    return (-(-M // 128), -(-K // 128), 32, 16)
+
+
+def _mx4_outs(lead, K, out, device):
+    """Codes [*lead, K/2] and scales for an MX4 result, new or checked."""
+    M = 1
+    for n in lead:
+        M *= n
+    if out is None:
+        return [torch.empty((*lead, K // 2), dtype=torch.uint8, device=device),
+                torch.empty(mx4_scale_shape(M, K), dtype=torch.uint8, device=device)]
+    q, sf = out
+    for t, name in ((q, "codes"), (sf, "scales")):
+        if t.dtype != torch.uint8:
+            raise ValueError(f"{name} must be uint8, got {t.dtype}")
+    return [_sized(q, (*lead, K // 2), "codes"), _sized(sf, mx4_scale_shape(M, K), "scales")]
+
+
+def group_norm_act_mx4(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str = "relu",
+                       out=None, workspace=None, stream=None):
+    """group_norm_act quantised to MX4: (codes [B, H, W, C/2], scales), the
+    operand of conv1x1_bias_add_act_mx4."""
+    return tuple(_norm("group_norm_act_mx4", x, gamma, beta, G, eps, r, act,
+                       lambda B, H, W, C, device: _mx4_outs((B, H, W), C, out, device),
+                       workspace, stream))
+
+
+def x1cb_mx4_scale_size(M: int, K: int) -> int:
+    return int(lib().x1cb_mx4_scale_size(int(M), int(K)))
+
+
+def x1cb_quantize_mx4(x, out=None, stream=None):
+    """x [..., K] float32, bfloat16 or float16 -> MX4 (codes [..., K/2] uint8,
+    scales [ceil(M/128), ceil(K/128), 32, 16] uint8), M the product of the
+    leading sizes; K % 32 == 0."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    *lead, K = x.shape
+    dt = _dtype(x.dtype, "x")
+    with _same_device(x):
+        st = _stream(stream, x.device)
+        with _alloc_on(stream, x.device):
+            q, sf = _mx4_outs(lead, K, out, x.device)
+        _same_device(x, q, sf)
+        status = lib().x1cb_quantize_mx4(_dev(x, x.dtype, "x"), dt, _dev(q, torch.uint8, "codes"),
+                                         _dev(sf, torch.uint8, "scales"),
+                                         x.numel() // K if K else 0, K, st)
+    _check(status, "x1cb_quantize_mx4")
+    return q, sf
+
+
+def x1cb_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None, stream=None):
+    """MX4 (codes [..., K/2], scales) -> values [..., K] of `dtype`."""
+    if not isinstance(q, torch.Tensor) or q.dim() < 1:
+        raise ValueError("codes must be [..., K/2]")
+    *lead, half = q.shape
+    dt, M, K = _dtype(dtype, "dtype"), q.numel() // half if half else 0, 2 * half
+    _sized(sf, mx4_scale_shape(M, K), "scales")
+    with _same_device(q, sf, out):
+        st = _stream(stream, q.device)
+        with _alloc_on(stream, q.device):
+            if out is None:
+                out = torch.empty((*lead, K), dtype=dtype, device=q.device)
+        _sized(out, (*lead, K), "out")
+        status = lib().x1cb_dequantize_mx4(_dev(q, torch.uint8, "codes"),
+                                           _dev(sf, torch.uint8, "scales"),
+                                           _dev(out, dtype, "out"), dt, M, K, st)
+    _check(status, "x1cb_dequantize_mx4")
+    return out
+
+
+def conv1x1_bias_add_act_mx4(x, xs, w, ws, bias=None, r=None, act: str = "relu",
+                             dtype=torch.bfloat16, out=None, stream=None):
+    """Fused 1x1 conv of MX4 operands + bias (+ shortcut Sum when r is given) +
+    activation; with H = W = 1 a fully connected layer.
+
+    x [B, H, W, Ic/2], xs MX4 activations; w [Oc, Ic/2], ws MX4 weights; bias
+    [Oc] float32 or None; r, out [B, H, W, Oc] of `dtype` (float32, bfloat16 or
+    float16)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError("x must be [B, H, W, Ic/2]")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be [Oc, Ic/2]")
+    B, H, W, half = x.shape
+    Oc, Ic = w.shape[0], 2 * half
+    dt, a = _dtype(dtype, "dtype"), _act(act)
+    _sized(w, (Oc, half), "w")
+    _sized(xs, mx4_scale_shape(B * H * W, Ic), "xs")
+    _sized(ws, mx4_scale_shape(Oc, Ic), "ws")
+    _sized(bias, (Oc,), "bias")
+    _sized(r, (B, H, W, Oc), "r")
+    with _same_device(x, xs, w, ws, bias, r, out):
+        st = _stream(stream, x.device)
+        with _alloc_on(stream, x.device):
+            if out is None:
+                out = torch.empty((B, H, W, Oc), dtype=dtype, device=x.device)
+        _sized(out, (B, H, W, Oc), "out")
+        status = lib().conv1x1_bias_add_act_mx4(
+            _dev(x, torch.uint8, "x"), _dev(xs, torch.uint8, "xs"), _dev(w, torch.uint8, "w"),
+            _dev(ws, torch.uint8, "ws"), _dev(bias, torch.float32, "bias"), _dev(r, dtype, "r"),
+            a, _dev(out, dtype, "out"), dt, B, H, W, Ic, Oc, st)
+    _check(status, "conv1x1_bias_add_act_mx4")
     return out
 
 

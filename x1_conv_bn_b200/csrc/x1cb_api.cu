@@ -14,6 +14,40 @@
 #include "x1cb_internal.h"
 
 namespace x1cb {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Every operand must be memory of the current device: the kernels launch on
+// the current device, and a pointer into another GPU (or into host memory)
+// would be read through a peer or host mapping, or fault.  NULL entries are
+// skipped (optional operands).
+int check_resident(std::initializer_list<const void *> ptrs)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return X1CB_ERR_CUDA;
+    for (const void *q : ptrs) {
+        if (!q)
+            continue;
+        cudaPointerAttributes a;
+        if (cudaPointerGetAttributes(&a, q) != cudaSuccess) {
+            cudaGetLastError();  // not sticky: clear it for later calls
+            return X1CB_ERR_DEVICE;
+        }
+        if ((a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) || a.device != dev)
+            return X1CB_ERR_DEVICE;
+    }
+    return X1CB_OK;
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    if (!a || !b || na == 0 || nb == 0)
+        return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + nb && b0 < a0 + na;
+}
+
 namespace {
 
 std::atomic<unsigned long long> g_wait_limit_ns{0};
@@ -93,39 +127,6 @@ found:
     const unsigned long long lim = g_wait_limit_ns.load();
     p.wait_limit_ns = lim ? lim : kDefaultWaitNs;
     return X1CB_OK;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Every operand must be memory of the current device: the kernels launch on
-// the current device, and a pointer into another GPU (or into host memory)
-// would be read through a peer or host mapping, or fault.  NULL entries are
-// skipped (optional operands).
-int check_resident(std::initializer_list<const void *> ptrs)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return X1CB_ERR_CUDA;
-    for (const void *q : ptrs) {
-        if (!q)
-            continue;
-        cudaPointerAttributes a;
-        if (cudaPointerGetAttributes(&a, q) != cudaSuccess) {
-            cudaGetLastError();  // not sticky: clear it for later calls
-            return X1CB_ERR_DEVICE;
-        }
-        if ((a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) || a.device != dev)
-            return X1CB_ERR_DEVICE;
-    }
-    return X1CB_OK;
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb)
-{
-    if (!a || !b || na == 0 || nb == 0)
-        return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + nb && b0 < a0 + na;
 }
 
 // Checks shared by the convolution entry points.
@@ -283,6 +284,16 @@ int device_info_check()
 }
 
 }  // namespace
+
+int current_sms(int &sms) { return device_info(sms); }
+
+unsigned long long wait_limit_ns()
+{
+    const unsigned long long lim = g_wait_limit_ns.load();
+    return lim ? lim : kDefaultWaitNs;
+}
+
+int debug_inject() { return g_inject.load(); }
 
 int bottleneck_chain(const int8_t *x, const int8_t *w1, const int32_t *b1, const int32_t *m1,
                      const int8_t *w2, const int32_t *b2, const int32_t *m2, const int8_t *w3,

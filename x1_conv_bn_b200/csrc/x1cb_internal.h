@@ -3,12 +3,24 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/x1cb.h"
 #include "x1cb_plan.h"
 
 namespace x1cb {
+
+// Argument checks shared by the entry points (x1cb_api.cu).
+bool aligned16(const void *p);
+int check_resident(std::initializer_list<const void *> ptrs);
+bool overlap(const void *a, size_t na, const void *b, size_t nb);
+// SMs of the current device (X1CB_ERR_ARCH unless it is an sm_100), the limit
+// of in-kernel waits, and the armed test hook.
+int current_sms(int &sms);
+unsigned long long wait_limit_ns();
+int debug_inject();
 
 void choose_tile(int B, int Wp, int Hp, int kb, int &tw, int &th, int &tg);
 void choose_halo_tile(int B, int H, int W, int &th, int &tg);
@@ -74,5 +86,35 @@ int launch_pack_stem(const int8_t *nhwc, int8_t *folded, int B, int H, int W, in
                      cudaStream_t s);
 int launch_pack_stem_weight(const int8_t *oihw, int8_t *blk, int Oc, int Cin, int R,
                             cudaStream_t s);
+
+// Floating-point operators (x1cb_norm.cu, x1cb_mx4.cu); the arguments have
+// passed the checks of x1cb_float.cu.
+enum NormOut { kNormSame = 0, kNormI8 = 1, kNormMx4 = 2 };
+struct NormCall {
+    const void *x, *r;
+    const float *gamma, *beta;
+    void *y;        // same type as x, int8 NC/32HW32, or the MX4 codes
+    uint8_t *sf;    // MX4 scales
+    float *ws;      // norm_workspace_floats() floats (NULL when 0)
+    float eps, q_mul;
+    int dtype, out, act;
+    int B, HW, C, G;
+};
+size_t norm_workspace_floats(int dtype, int B, int HW, int C, int G);
+int launch_norm(const NormCall &c, cudaStream_t s);
+int launch_quantize_mx4(const void *x, int dtype, uint8_t *q, uint8_t *sf, long long M, int K,
+                        cudaStream_t s);
+int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtype, long long M,
+                          int K, cudaStream_t s);
+struct Mx4Call {
+    const uint8_t *x, *xs, *w, *ws;
+    const float *bias;
+    const void *r;
+    void *out;
+    int dtype, act;
+    long long M;
+    int K, N;
+};
+int launch_conv_mx4(const Mx4Call &c, cudaStream_t s);
 
 }  // namespace x1cb
