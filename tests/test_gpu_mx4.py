@@ -274,6 +274,30 @@ def test_conv_capture_and_streams(shape):
     assert torch.equal(a, want) and torch.equal(b, want2)
 
 
+@pytest.mark.parametrize("shape", [(1, 20, 20, 512, 256)])
+def test_conv_bounded_wait(shape):
+    """A wait that runs out is reported, and the next call works."""
+    B, H, W, Ic, Oc = shape
+    g = _gen(13)
+    (x, xs), _ = _operand(B * H * W, Ic, g)
+    (w, ws), _ = _operand(Oc, Ic, g)
+    x = x.view(B, H, W, Ic // 2)
+    want = X.conv1x1_bias_add_act_mx4(x, xs, w, ws)
+    _clean()
+    try:
+        X.x1cb_set_wait_limit_ns(20_000_000)
+        X.x1cb_debug_inject(1)
+        X.conv1x1_bias_add_act_mx4(x, xs, w, ws)
+        st, bits = X.x1cb_last_device_error(clear=True)
+        assert st == X.X1CB_ERR_TIMEOUT and bits & 2
+    finally:
+        X.x1cb_debug_inject(0)
+        X.x1cb_set_wait_limit_ns(0)
+    got = X.conv1x1_bias_add_act_mx4(x, xs, w, ws)
+    _clean()
+    assert torch.equal(got, want)
+
+
 # ---- together --------------------------------------------------------------------
 
 @pytest.mark.parametrize("shape", [(2, 14, 14, 256, 32, 64), (1, 1, 1, 2048, 32, 1000),

@@ -116,5 +116,6 @@ struct Mx4Call {
     int K, N;
 };
 int launch_conv_mx4(const Mx4Call &c, cudaStream_t s);
+int launch_conv_mx4_tiles(const Mx4Call &c, cudaStream_t s);  // x1cb_mxconv.cu
 
 }  // namespace x1cb

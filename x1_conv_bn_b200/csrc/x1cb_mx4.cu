@@ -215,6 +215,8 @@ int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtyp
 
 int launch_conv_mx4(const Mx4Call &c, cudaStream_t s)
 {
+    if (c.M > 8)
+        return launch_conv_mx4_tiles(c, s);
     Mx4Call a = c;
     const void *k = c.dtype == X1CB_F32    ? reinterpret_cast<const void *>(conv_rows_kernel<float>)
                     : c.dtype == X1CB_BF16 ? reinterpret_cast<const void *>(conv_rows_kernel<__nv_bfloat16>)

@@ -676,4 +676,95 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
         : "memory");
 }
 
+// ---- MX4 operands (kind::mxf4) -------------------------------------------------
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar,
+                                            int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+// Contiguous copy (16-byte aligned on both sides, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// Shared-memory matrix descriptor for a K-major operand stored with the
+// 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.  A start
+// moved by 32 bytes is the next K step of 64 four-bit elements.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
+    d |= static_cast<uint64_t>(1) << 16;                  // leading offset (unused here)
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;          // between 8-row groups
+    d |= static_cast<uint64_t>(1) << 46;                  // descriptor version
+    d |= static_cast<uint64_t>(2) << 61;                  // 128-byte swizzle
+    return d;
+}
+
+// Descriptor of one 512-byte tile of scales (32 rows of 16 bytes) for tmem_cp_scales.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;          // leading offset (unused here)
+    d |= static_cast<uint64_t>(128 >> 4) << 32;   // between 8-row groups
+    d |= static_cast<uint64_t>(1) << 46;
+    return d;                                     // no swizzle
+}
+
+// Instruction descriptor: e2m1 x e2m1 -> f32 with e8m0 scales, both operands
+// K-major, M x N; sf: which bytes of each scale word this K step uses (0 or 2).
+__host__ __device__ constexpr uint32_t idesc_mx4(uint32_t M, uint32_t N, uint32_t sf)
+{
+    return (sf << 4)             // B scale bytes
+           | (1u << 7)           // A: e2m1
+           | (1u << 10)          // B: e2m1
+           | ((N >> 3) << 17)    // N
+           | (1u << 23)          // scales: e8m0
+           | ((M >> 4) << 24)    // M
+           | (sf << 29);         // A scale bytes
+}
+
+// Copies one 512-byte scale tile from shared memory into four TMEM columns:
+// column j, lane i (repeated in the four lane quarters) = the four scale bytes
+// of row 32 j + i.  Warp-wide with an elected lane, in order before the MMAs
+// that the same lane issues next.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(sdesc)
+        : "memory");
+}
+
+// One MMA step of K = 64: D (+)= A x B with one scale per row and 32 elements.
+// Warp-wide with an elected lane; accumulate = 0 overwrites D.
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "[%5], [%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+
 }  // namespace x1cb
