@@ -455,24 +455,63 @@ def _act(act: str) -> int:
 
 
 def _sized(t: Optional[torch.Tensor], shape, name: str):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
-def _alloc_on(stream, device):
-    """Context in which outputs and workspaces are allocated: the stream the
-    call runs on, so that the allocator never hands out memory that work on
-    another stream still uses, or takes back a workspace too early."""
+def _cuda_index(t, name: str) -> int:
+    """Index of the GPU that the call's first operand lives on."""
+    d = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return d
+
+
+def _ptr(t, dtype, index: int, name: str):
+    """Device address of an operand (None: NULL) after the checks of _dev, and
+    that it lives on GPU `index`."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _raw_stream(stream, index: int) -> int:
     if stream is None:
-        return torch.cuda.stream(None)
+        return torch._C._cuda_getCurrentRawStream(index)
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, operands on cuda:{index}")
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype, index: int, stream):
+    """A new tensor, allocated on the stream the call runs on, so that the
+    allocator never hands out memory that work on another stream still uses, or
+    takes back a workspace too early."""
+    device = torch.device("cuda", index)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if raw == 0:  # the legacy default stream
-            stream = torch.cuda.default_stream(device)
-        else:
-            stream = torch.cuda.ExternalStream(raw, device=device)
-    return torch.cuda.stream(stream)
+        raw = _raw_stream(stream, index)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw \
+            else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(what: str, index: int, *args):
+    """Runs the library call with GPU `index` current."""
+    if torch.cuda.current_device() == index:
+        status = getattr(lib(), what)(*args)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib(), what)(*args)
+    if status != X1CB_OK:
+        raise X1cbError(status, what)
 
 
 def group_norm_workspace_size(dtype, B: int, H: int, W: int, C: int, G: int) -> int:
@@ -480,31 +519,27 @@ def group_norm_workspace_size(dtype, B: int, H: int, W: int, C: int, G: int) -> 
     return int(lib().group_norm_workspace_size(_dtype(dtype, "dtype"), B, H, W, C, G))
 
 
-def _norm(what, x, gamma, beta, G, eps, r, act, outs, workspace, stream, q_mul=None):
-    """Shared by the group_norm_act calls; outs(B, H, W, C, device) allocates or
+def _norm(what, x, gamma, beta, G, eps, r, act, outs, workspace, stream, q_mul=()):
+    """Shared by the group_norm_act calls; outs(shape, index) allocates or
     checks the outputs."""
     if not isinstance(x, torch.Tensor) or x.dim() != 4:
         raise ValueError("x must be [B, H, W, C]")
-    B, H, W, C = x.shape
-    dt, a = _dtype(x.dtype, "x"), _act(act)
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        _sized(t, (C,), name)
-    _sized(r, x.shape, "r")
-    need = group_norm_workspace_size(x.dtype, B, H, W, C, int(G))
-    with _same_device(x, gamma, beta, r, workspace):
-        st = _stream(stream, x.device)
-        with _alloc_on(stream, x.device):
-            ys = outs(B, H, W, C, x.device)
-            if workspace is None and need:
-                workspace = torch.empty(need, dtype=torch.int8, device=x.device)
-        _same_device(x, *ys)
-        status = getattr(lib(), what)(
-            _dev(x, x.dtype, "x"), dt, _dev(gamma, torch.float32, "gamma"),
-            _dev(beta, torch.float32, "beta"), _dev(r, x.dtype, "r"), a, float(eps),
-            *([] if q_mul is None else [float(q_mul)]), *[_dev(y, y.dtype, "out") for y in ys],
-            _dev(workspace, torch.int8, "workspace"),
-            0 if workspace is None else workspace.numel(), B, H, W, C, int(G), st)
-    _check(status, what)
+    shape = x.shape
+    B, H, W, C = shape
+    dt, a, index, G = _dtype(x.dtype, "x"), _act(act), _cuda_index(x, "x"), int(G)
+    _sized(gamma, (C,), "gamma")
+    _sized(beta, (C,), "beta")
+    _sized(r, shape, "r")
+    ys = outs(shape, index)
+    need = lib().group_norm_workspace_size(dt, B, H, W, C, G)
+    if workspace is None and need:
+        workspace = _empty(need, torch.int8, index, stream)
+    _call(what, index, _ptr(x, x.dtype, index, "x"), dt, _ptr(gamma, torch.float32, index, "gamma"),
+          _ptr(beta, torch.float32, index, "beta"), _ptr(r, x.dtype, index, "r"), a, eps, *q_mul,
+          *[_ptr(y, y.dtype, index, "out") for y in ys],
+          _ptr(workspace, torch.int8, index, "workspace"),
+          0 if workspace is None else workspace.numel(), B, H, W, C, G,
+          _raw_stream(stream, index))
     return ys
 
 
@@ -514,12 +549,12 @@ def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str =
 
     x, r, out [B, H, W, C] float32, bfloat16 or float16; gamma, beta [C]
     float32 or None; G groups; act "none", "relu" or "silu"."""
-    def outs(B, H, W, C, device):
+    def outs(shape, index):
         if out is None:
-            return [torch.empty((B, H, W, C), dtype=x.dtype, device=device)]
+            return (_empty(shape, x.dtype, index, stream),)
         if out.dtype != x.dtype:
             raise ValueError(f"out must be {x.dtype}, got {out.dtype}")
-        return [_sized(out, x.shape, "out")]
+        return (_sized(out, shape, "out"),)
 
     return _norm("group_norm_act", x, gamma, beta, G, eps, r, act, outs, workspace, stream)[0]
 
@@ -528,16 +563,17 @@ def group_norm_act_i8(x, gamma, beta, G: int, q_mul: float, eps: float = 1e-5, r
                       act: str = "relu", out=None, workspace=None, stream=None):
     """group_norm_act quantised for the int8 convolutions: clamp(rint(y * q_mul),
     -128, 127) as NC/32HW32 [B, C/32, H, W, 32]."""
-    def outs(B, H, W, C, device):
+    def outs(shape, index):
+        B, H, W, C = shape
         shape = (B, C // 32, H, W, 32)
         if out is None:
-            return [torch.empty(shape, dtype=torch.int8, device=device)]
+            return (_empty(shape, torch.int8, index, stream),)
         if out.dtype != torch.int8:
             raise ValueError(f"out must be int8, got {out.dtype}")
-        return [_sized(out, shape, "out")]
+        return (_sized(out, shape, "out"),)
 
     return _norm("group_norm_act_i8", x, gamma, beta, G, eps, r, act, outs, workspace, stream,
-                 q_mul)[0]
+                 (float(q_mul),))[0]
 
 
 def mx4_scale_shape(M: int, K: int):
@@ -545,28 +581,28 @@ def mx4_scale_shape(M: int, K: int):
     return (-(-M // 128), -(-K // 128), 32, 16)
 
 
-def _mx4_outs(lead, K, out, device):
+def _mx4_outs(lead, M, K, out, index, stream):
     """Codes [*lead, K/2] and scales for an MX4 result, new or checked."""
-    M = 1
-    for n in lead:
-        M *= n
+    shape, scales = (*lead, K // 2), mx4_scale_shape(M, K)
     if out is None:
-        return [torch.empty((*lead, K // 2), dtype=torch.uint8, device=device),
-                torch.empty(mx4_scale_shape(M, K), dtype=torch.uint8, device=device)]
+        return (_empty(shape, torch.uint8, index, stream),
+                _empty(scales, torch.uint8, index, stream))
     q, sf = out
     for t, name in ((q, "codes"), (sf, "scales")):
         if t.dtype != torch.uint8:
             raise ValueError(f"{name} must be uint8, got {t.dtype}")
-    return [_sized(q, (*lead, K // 2), "codes"), _sized(sf, mx4_scale_shape(M, K), "scales")]
+    return (_sized(q, shape, "codes"), _sized(sf, scales, "scales"))
 
 
 def group_norm_act_mx4(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str = "relu",
                        out=None, workspace=None, stream=None):
     """group_norm_act quantised to MX4: (codes [B, H, W, C/2], scales), the
     operand of conv1x1_bias_add_act_mx4."""
-    return tuple(_norm("group_norm_act_mx4", x, gamma, beta, G, eps, r, act,
-                       lambda B, H, W, C, device: _mx4_outs((B, H, W), C, out, device),
-                       workspace, stream))
+    def outs(shape, index):
+        B, H, W, C = shape
+        return _mx4_outs((B, H, W), B * H * W, C, out, index, stream)
+
+    return _norm("group_norm_act_mx4", x, gamma, beta, G, eps, r, act, outs, workspace, stream)
 
 
 def x1cb_mx4_scale_size(M: int, K: int) -> int:
@@ -580,16 +616,11 @@ def x1cb_quantize_mx4(x, out=None, stream=None):
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be [..., K]")
     *lead, K = x.shape
-    dt = _dtype(x.dtype, "x")
-    with _same_device(x):
-        st = _stream(stream, x.device)
-        with _alloc_on(stream, x.device):
-            q, sf = _mx4_outs(lead, K, out, x.device)
-        _same_device(x, q, sf)
-        status = lib().x1cb_quantize_mx4(_dev(x, x.dtype, "x"), dt, _dev(q, torch.uint8, "codes"),
-                                         _dev(sf, torch.uint8, "scales"),
-                                         x.numel() // K if K else 0, K, st)
-    _check(status, "x1cb_quantize_mx4")
+    dt, index, M = _dtype(x.dtype, "x"), _cuda_index(x, "x"), x.numel() // K if K else 0
+    q, sf = _mx4_outs(lead, M, K, out, index, stream)
+    _call("x1cb_quantize_mx4", index, _ptr(x, x.dtype, index, "x"), dt,
+          _ptr(q, torch.uint8, index, "codes"), _ptr(sf, torch.uint8, index, "scales"), M, K,
+          _raw_stream(stream, index))
     return q, sf
 
 
@@ -600,16 +631,13 @@ def x1cb_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None, stream=None):
     *lead, half = q.shape
     dt, M, K = _dtype(dtype, "dtype"), q.numel() // half if half else 0, 2 * half
     _sized(sf, mx4_scale_shape(M, K), "scales")
-    with _same_device(q, sf, out):
-        st = _stream(stream, q.device)
-        with _alloc_on(stream, q.device):
-            if out is None:
-                out = torch.empty((*lead, K), dtype=dtype, device=q.device)
-        _sized(out, (*lead, K), "out")
-        status = lib().x1cb_dequantize_mx4(_dev(q, torch.uint8, "codes"),
-                                           _dev(sf, torch.uint8, "scales"),
-                                           _dev(out, dtype, "out"), dt, M, K, st)
-    _check(status, "x1cb_dequantize_mx4")
+    index = _cuda_index(q, "codes")
+    if out is None:
+        out = _empty((*lead, K), dtype, index, stream)
+    _sized(out, (*lead, K), "out")
+    _call("x1cb_dequantize_mx4", index, _ptr(q, torch.uint8, index, "codes"),
+          _ptr(sf, torch.uint8, index, "scales"), _ptr(out, dtype, index, "out"), dt, M, K,
+          _raw_stream(stream, index))
     return out
 
 
@@ -626,24 +654,22 @@ def conv1x1_bias_add_act_mx4(x, xs, w, ws, bias=None, r=None, act: str = "relu",
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be [Oc, Ic/2]")
     B, H, W, half = x.shape
-    Oc, Ic = w.shape[0], 2 * half
+    Oc, Ic, shape = w.shape[0], 2 * half, (B, H, W, w.shape[0])
     dt, a = _dtype(dtype, "dtype"), _act(act)
     _sized(w, (Oc, half), "w")
     _sized(xs, mx4_scale_shape(B * H * W, Ic), "xs")
     _sized(ws, mx4_scale_shape(Oc, Ic), "ws")
     _sized(bias, (Oc,), "bias")
-    _sized(r, (B, H, W, Oc), "r")
-    with _same_device(x, xs, w, ws, bias, r, out):
-        st = _stream(stream, x.device)
-        with _alloc_on(stream, x.device):
-            if out is None:
-                out = torch.empty((B, H, W, Oc), dtype=dtype, device=x.device)
-        _sized(out, (B, H, W, Oc), "out")
-        status = lib().conv1x1_bias_add_act_mx4(
-            _dev(x, torch.uint8, "x"), _dev(xs, torch.uint8, "xs"), _dev(w, torch.uint8, "w"),
-            _dev(ws, torch.uint8, "ws"), _dev(bias, torch.float32, "bias"), _dev(r, dtype, "r"),
-            a, _dev(out, dtype, "out"), dt, B, H, W, Ic, Oc, st)
-    _check(status, "conv1x1_bias_add_act_mx4")
+    _sized(r, shape, "r")
+    index = _cuda_index(x, "x")
+    if out is None:
+        out = _empty(shape, dtype, index, stream)
+    _sized(out, shape, "out")
+    u8 = torch.uint8
+    _call("conv1x1_bias_add_act_mx4", index, _ptr(x, u8, index, "x"), _ptr(xs, u8, index, "xs"),
+          _ptr(w, u8, index, "w"), _ptr(ws, u8, index, "ws"),
+          _ptr(bias, torch.float32, index, "bias"), _ptr(r, dtype, index, "r"), a,
+          _ptr(out, dtype, index, "out"), dt, B, H, W, Ic, Oc, _raw_stream(stream, index))
     return out
 
 
