@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/x1cb.h"
 
@@ -48,14 +49,163 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 }
 template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// v < 0 is false for NaN, which therefore passes through ReLU.
+// Two floats in a 64-bit register: add, multiply-add and multiply work on both
+// at once (sm_100), each rounded as the scalar operation.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float x, float y)
+{
+    F2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 un2(F2 v)
+{
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Pairs of a vector of V elements; an odd single element leaves the upper half 0.
+template <int V> constexpr int kPairs = (V + 1) / 2;
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V> &v, F2 (&f)[kPairs<V>])
+{
+    if constexpr (V == 1) {
+        f[0] = f2(to_f(v.e[0]), 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const uint32_t w = reinterpret_cast<const uint32_t *>(&v)[i];
+                f[i] = f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const float2 t = __half22float2(reinterpret_cast<const __half2 *>(&v)[i]);
+                f[i] = f2(t.x, t.y);
+            } else {
+                f[i] = f2(v.e[2 * i], v.e[2 * i + 1]);
+            }
+        }
+    }
+}
+
+// Two floats -> two elements of 16 bits; RELU: negative results become 0 (NaN stays).
+template <typename T, bool RELU> __device__ __forceinline__ uint32_t pack2(float x, float y)
+{
+    uint32_t d;
+    if constexpr (std::is_same<T, __half>::value) {
+        if constexpr (RELU)
+            asm("cvt.rn.relu.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+        else
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+    } else {
+        if constexpr (RELU)
+            asm("cvt.rn.relu.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+        else
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+    }
+    return d;
+}
+
+// NaN stays NaN.
+__device__ __forceinline__ float relu(float v)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(d) : "f"(v));
+    return d;
+}
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+
 __device__ __forceinline__ float activate(float v, int act)
 {
-    if (act == X1CB_ACT_RELU)
-        return v < 0.f ? 0.f : v;
-    if (act == X1CB_ACT_SILU)
-        return __fdividef(v, 1.f + __expf(-v));
+    return act == X1CB_ACT_RELU ? relu(v) : act == X1CB_ACT_SILU ? silu(v) : v;
+}
+
+template <int V> __device__ __forceinline__ void activate(float (&y)[V], int act)
+{
+    if (act == X1CB_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            y[i] = relu(y[i]);
+    } else if (act == X1CB_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            y[i] = silu(y[i]);
+    }
+}
+
+// act(y) rounded to T, in one pass: ReLU is part of the 16-bit conversions.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> finish(const F2 (&f)[kPairs<V>], int act)
+{
+    Vec<T, V> v;
+    if constexpr (V == 1) {
+        v.e[0] = from_f<T>(activate(un2(f[0]).x, act));
+    } else if constexpr (sizeof(T) == 4) {
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 t = un2(f[i]);
+            y[2 * i] = t.x;
+            y[2 * i + 1] = t.y;
+        }
+        activate(y, act);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v.e[i] = y[i];
+    } else {
+        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+        if (act == X1CB_ACT_RELU) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 t = un2(f[i]);
+                w[i] = pack2<T, true>(t.x, t.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                float2 t = un2(f[i]);
+                if (act == X1CB_ACT_SILU)
+                    t = make_float2(silu(t.x), silu(t.y));
+                w[i] = pack2<T, false>(t.x, t.y);
+            }
+        }
+    }
     return v;
+}
+
+// Copy of N bytes from global to shared memory that completes in the thread's
+// bulk of asynchronous copies (commit, then wait).
+template <int N> __device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(N)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Byte of the scale of (row, block) in an MX4 scale array whose rows have kt =

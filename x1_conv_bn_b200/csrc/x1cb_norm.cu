@@ -1,14 +1,15 @@
 // Group norm + shortcut Sum + activation, channels last, with floating-point,
 // int8 NC/32HW32 or MX4 output.
 //
-// Statistics: a thread owns V neighbouring channels and walks down the pixels.
-// Per channel it sums d = x - k and d^2 about the first value k it met, which
-// gives its mean and its sum of squares about the mean, M2 = sum d^2 -
+// Statistics: a thread owns V neighbouring channels and walks down up to 64
+// pixels.  Per channel it sums d = x - k and d^2 about the first value k it met,
+// which gives its mean and its sum of squares about the mean, M2 = sum d^2 -
 // (sum d)^2/n.  k being one of the n values, n (mean - k)^2 <= n M2, so the
 // subtraction costs at most a factor n of the relative rounding error, however
-// far the data lies from zero; n is kept at or below 64 by folding the sums
-// into a running (mean, M2) after 64 pixels.  Partial results are joined in a
-// fixed order: the mean of the parts, then M2 + n (mean - joint mean)^2 summed.
+// far the data lies from zero.  A block joins its threads' (n, mean, M2) about
+// the mean R of one of them, S1 = sum n (mean - R) and S2 = sum M2 + n (mean -
+// R)^2, by the same argument with the number of threads; parts of different
+// blocks are joined in 64 bits.  All in a fixed order.
 //
 // Two forms.  Where an image (or a slice of its channels that holds whole
 // groups) fits the shared memory of a cluster of up to eight CTAs, one launch
@@ -33,7 +34,7 @@ namespace x1cb {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kFold = 64;  // pixels a channel's shifted sums run over
+constexpr int kFold = 64;  // pixels a thread's shifted sums run over at most
 constexpr int kBatch = 4;  // vectors a thread has in flight
 
 struct NormArgs {
@@ -50,61 +51,70 @@ struct NormArgs {
     int b0;             // first image of the launch (two-launch form)
     int Cs, slices;     // channels per slice, slices (cluster form)
     int iters;          // pixels per thread (cluster form)
+    int stage_r;        // the shortcut goes through shared memory too
+    double count;       // values per group and image: HW * cg
 };
 
-// (mean, M2) of the values seen so far, and the shifted sums of the current run.
-template <int V> struct Running {
-    float mean[V], m2[V], k[V], s[V], q[V];
-    int n = 0, run = 0;
+// Shifted sums of a thread's V channels over n pixels.
+template <int V> struct Sums {
+    F2 k[kPairs<V>], s[kPairs<V>], q[kPairs<V>];  // -first value, sum d, sum d^2
 
-    __device__ __forceinline__ void add(const float (&x)[V])
+    template <typename T> __device__ __forceinline__ void start(const Vec<T, V> &v)
     {
-        if (run == 0) {
+        unpack<T, V>(v, k);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                k[i] = x[i];
-                s[i] = q[i] = 0.f;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = x[i] - k[i];
-                s[i] += d;
-                q[i] = fmaf(d, d, q[i]);
-            }
+        for (int i = 0; i < kPairs<V>; ++i) {
+            const float2 t = un2(k[i]);
+            k[i] = f2(-t.x, -t.y);
+            s[i] = q[i] = f2(0.f, 0.f);
         }
-        if (++run == kFold)
-            fold();
     }
-    __device__ __forceinline__ void fold()
+    template <typename T> __device__ __forceinline__ void add(const Vec<T, V> &v)
     {
-        if (run == 0)
-            return;
-        const float inv = 1.f / static_cast<float>(run);
-        const float w = static_cast<float>(run) / static_cast<float>(n + run);
+        F2 f[kPairs<V>];
+        unpack<T, V>(v, f);
+#pragma unroll
+        for (int i = 0; i < kPairs<V>; ++i) {
+            const F2 d = add2(f[i], k[i]);
+            s[i] = add2(s[i], d);
+            q[i] = fma2(d, d, q[i]);
+        }
+    }
+    // Writes (mean, M2) of each channel, or of all V together (one), to out.
+    __device__ __forceinline__ void write(int n, bool one, float2 *out) const
+    {
+        const float inv = n ? 1.f / static_cast<float>(n) : 0.f;
+        float mean[V], m2[V], off = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float ms = s[i] * inv;
-            const float rm = k[i] + ms;
-            const float r2 = fmaxf(fmaf(-ms, s[i], q[i]), 0.f);
-            if (n == 0) {
-                mean[i] = rm;
-                m2[i] = r2;
-            } else {
-                const float d = rm - mean[i];
-                mean[i] = fmaf(d, w, mean[i]);
-                m2[i] += r2 + d * d * (static_cast<float>(n) * w);
-            }
+            const float2 kk = un2(k[i / 2]), ss = un2(s[i / 2]), qq = un2(q[i / 2]);
+            const float si = i % 2 ? ss.y : ss.x, qi = i % 2 ? qq.y : qq.x;
+            const float ms = si * inv;
+            mean[i] = (i % 2 ? -kk.y : -kk.x) + ms;
+            m2[i] = fmaxf(fmaf(-ms, si, qi), 0.f);
+            off += mean[i] - mean[0];
         }
-        n += run;
-        run = 0;
+        if (!one) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                out[i] = make_float2(mean[i], m2[i]);
+            return;
+        }
+        const float all = fmaf(off, 1.f / V, mean[0]);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float d = mean[i] - all;
+            sum += fmaf(d * d, static_cast<float>(n), m2[i]);
+        }
+        out[0] = make_float2(all, sum);
     }
 };
 
-__device__ __forceinline__ double warp_sum(double v)
+// Sum over the `width` lanes (a power of two) around each lane.
+template <typename T> __device__ __forceinline__ T lanes_sum(T v, int width)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = width >> 1; o > 0; o >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
@@ -113,181 +123,233 @@ struct Joined {
     double mean, m2;
 };
 
-// Joins `count` parts of one group, part i of (mean, M2) and weight get(i, c):
-// the warp's lanes take the parts in turn.  In 64 bits: there are few parts,
-// and what is left of the 32-bit sums' rounding errors averages out over them.
-template <typename Get>
-__device__ __forceinline__ Joined warp_join(int count, int lane, const Get &get)
+// Joins the (mean, M2) that a block's threads wrote for one group: entry v of
+// pixel lane l at buf[l * pitch + v], v < width, each standing for n * each
+// values, n = px / lanes (+ 1 for the first px % lanes lanes).  The w lanes that
+// share the group take the pixel lanes in turn; whole warps call it.
+__device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int lanes, int pitch,
+                                               int width, int each, int w, bool active)
 {
-    double n = 0., sum = 0.;
-#pragma unroll 4
-    for (int i = lane; i < count; i += 32) {
-        float c;
-        const float2 p = get(i, c);
-        n += c;
-        sum += static_cast<double>(c) * p.x;
+    float s1 = 0.f, s2 = 0.f, ref = 0.f;
+    if (active) {
+        ref = buf[0].x;
+        const int base = px / lanes, more = px - base * lanes;
+        for (int l = threadIdx.x & (w - 1); l < lanes; l += w) {
+            const float n = static_cast<float>((base + (l < more)) * each);
+            if (n == 0.f)
+                break;
+            float t = 0.f, u = 0.f, m = 0.f;
+            const float2 *p = buf + l * pitch;
+            for (int v = 0; v < width; ++v) {
+                const float d = p[v].x - ref;
+                t += d;
+                u = fmaf(d, d, u);
+                m += p[v].y;
+            }
+            s1 = fmaf(n, t, s1);
+            s2 += fmaf(n, u, m);
+        }
     }
-    n = warp_sum(n);
-    const double mean = warp_sum(sum) / n;
-    double m2 = 0.;
-#pragma unroll 4
-    for (int i = lane; i < count; i += 32) {
-        float c;
-        const float2 p = get(i, c);
-        const double d = p.x - mean;
-        m2 += c * d * d + p.y;
-    }
-    return Joined{mean, warp_sum(m2)};
+    s1 = lanes_sum(s1, w);
+    s2 = lanes_sum(s2, w);
+    const double mean = s1 / (static_cast<double>(px) * (width * each));
+    return Joined{ref + mean, s2 - s1 * mean};
 }
 
-// What the normalisation needs of a group: 1/std, and the mean as a float and
-// the float's rounding error (which goes into the bias).
+// Lanes per group so that a block's threads cover all groups at once where they can.
+__device__ __forceinline__ int join_width(int groups)
+{
+    int w = 32;
+    while (w > 1 && w * groups > kBlock)
+        w >>= 1;
+    return w;
+}
+
+// What the normalisation needs of a group.
 struct Coef {
-    float mu, mu_low, rstd;
+    float mu, mu_low, rstd;  // the mean as a float and that float's rounding error
 };
-__device__ __forceinline__ Coef make_coef(const Joined &j, double n, float eps)
+__device__ __forceinline__ Coef make_coef(const Joined &j, double count, float eps)
 {
     Coef c;
     c.mu = static_cast<float>(j.mean);
     c.mu_low = static_cast<float>(j.mean - c.mu);
-    c.rstd = static_cast<float>(1. / sqrt(j.m2 / n + eps));
+    // 1/sqrt(v): a 32-bit estimate and one Newton step in 64 bits
+    const double v = fmax(j.m2, 0.) / count + eps;
+    const double r = 1.f / sqrtf(static_cast<float>(v));
+    c.rstd = static_cast<float>(r * (1.5 - 0.5 * v * r * r));
+    if (!(v >= 1e-30))
+        c.rstd = static_cast<float>(1. / sqrt(v));  // (also infinity, NaN)
+    else if (v > 1e30)
+        c.rstd = static_cast<float>(1. / sqrt(v));
     return c;
 }
 
-// y = (x - mu) * sc + be of V channels from c on; g0 the slice's first channel.
-template <int V> struct Affine {
-    float mu[V], sc[V], be[V];
-    __device__ __forceinline__ Affine(const NormArgs &a, const Coef *coef, int c0, int c)
+// The normalisation of V channels.  16-bit inputs: y = x * sc + be, be = beta -
+// mu * sc; what rounding be loses is far below the input's own step.  32-bit
+// inputs: y = (x - mu) * sc + be with the mean's low part in be.
+template <typename T, int V> struct Affine {
+    static constexpr bool kSub = sizeof(T) == 4;
+    F2 mu[kSub ? kPairs<V> : 1], sc[kPairs<V>], be[kPairs<V>];
+    // c: the first channel, cs: the same counted from the slice's first group
+    __device__ __forceinline__ Affine(const NormArgs &a, const Coef *coef, int c, int cs, bool one)
     {
+        float m[V + 1], s[V + 1], b[V + 1];
+        m[V] = s[V] = b[V] = 0.f;
+        int g = cs / a.cg, left = a.cg - (cs - g * a.cg);
+        Coef k = coef[g];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const Coef k = coef[(c + i) / a.cg];
-            const float gamma = a.gamma ? a.gamma[c0 + c + i] : 1.f;
-            mu[i] = k.mu;
-            sc[i] = k.rstd * gamma;
-            be[i] = (a.beta ? a.beta[c0 + c + i] : 0.f) - k.mu_low * sc[i];
+            if (!one && i > 0 && --left == 0) {
+                k = coef[++g];
+                left = a.cg;
+            }
+            s[i] = a.gamma ? k.rstd * a.gamma[c + i] : k.rstd;
+            const float beta = a.beta ? a.beta[c + i] : 0.f;
+            m[i] = -k.mu;
+            b[i] = kSub ? fmaf(-k.mu_low, s[i], beta)
+                        : static_cast<float>(beta - (static_cast<double>(k.mu) + k.mu_low) * s[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs<V>; ++i) {
+            if (kSub)
+                mu[i] = f2(m[2 * i], m[2 * i + 1]);
+            sc[i] = f2(s[2 * i], s[2 * i + 1]);
+            be[i] = f2(b[2 * i], b[2 * i + 1]);
         }
     }
-    template <typename T>
-    __device__ __forceinline__ void apply(const NormArgs &a, const Vec<T, V> &x, const Vec<T, V> *r,
-                                          float (&y)[V]) const
+    __device__ __forceinline__ void apply(const Vec<T, V> &x, const Vec<T, V> *r,
+                                          F2 (&y)[kPairs<V>]) const
     {
+        unpack<T, V>(x, y);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            y[i] = fmaf(to_f(x.e[i]) - mu[i], sc[i], be[i]);
+        for (int i = 0; i < kPairs<V>; ++i)
+            y[i] = fma2(kSub ? add2(y[i], mu[i]) : y[i], sc[i], be[i]);
         if (r) {
+            F2 f[kPairs<V>];
+            unpack<T, V>(*r, f);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                y[i] += to_f(r->e[i]);
+            for (int i = 0; i < kPairs<V>; ++i)
+                y[i] = add2(y[i], f[i]);
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            y[i] = activate(y[i], a.act);
     }
 };
 
 // Statistics of one chunk of pixels of one image: part[b][chunk][g].
 template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stats_kernel(NormArgs a)
 {
-    extern __shared__ float2 buf[];  // [lanes][C] (mean, M2) of each pixel lane and channel
+    extern __shared__ float2 buf[];  // (mean, M2) by pixel lane and vector or channel
     griddep_wait();
     const int b = a.b0 + blockIdx.y;
-    const int p0 = blockIdx.x * a.chunk, p1 = min(a.HW, p0 + a.chunk);
-    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(b) * a.HW * a.C;
+    const int p0 = blockIdx.x * a.chunk, px = min(a.HW - p0, a.chunk);
+    const bool one = a.cg % V == 0;
+    const int each = one ? V : 1, width = a.cg / each, pitch = a.C / each;
     const int pl = threadIdx.x / a.nv;
     if (pl < a.lanes) {
-        for (int cv = threadIdx.x - pl * a.nv; cv < a.nv; cv += kBlock) {
-            Running<V> st;
-            const T *xc = x + cv * V;
-            for (int p = p0 + pl; p < p1; p += kBatch * a.lanes) {
-                Vec<T, V> v[kBatch];
+        const int mine = px > pl ? (px - pl + a.lanes - 1) / a.lanes : 0;
+        const size_t step = static_cast<size_t>(a.lanes) * a.C;
+        for (int cv = threadIdx.x - pl * a.nv; cv < a.nv && mine > 0; cv += kBlock) {
+            const T *x = static_cast<const T *>(a.x) +
+                         (static_cast<size_t>(b) * a.HW + p0 + pl) * a.C + cv * V;
+            Sums<V> st;
+            Vec<T, V> v[kBatch];
+            for (int i0 = 0; i0 < mine; i0 += kBatch) {
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j)
-                    if (p + j * a.lanes < p1)
-                        v[j] = load_vec<T, V>(xc + static_cast<size_t>(p + j * a.lanes) * a.C);
+                    if (i0 + j < mine)
+                        v[j] = load_vec<T, V>(x + j * step);
+                x += kBatch * step;
+                if (i0 == 0)
+                    st.start(v[0]);
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    if (p + j * a.lanes < p1) {
-                        float f[V];
-#pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            f[i] = to_f(v[j].e[i]);
-                        st.add(f);
-                    }
-                }
+                for (int j = 0; j < kBatch; ++j)
+                    if (i0 + j < mine)
+                        st.add(v[j]);
             }
-            st.fold();
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                buf[pl * a.C + cv * V + i] =
-                    st.n ? make_float2(st.mean[i], st.m2[i]) : make_float2(0.f, 0.f);
+            st.write(mine, one, buf + (pl * a.nv + cv) * (V / each));
         }
     }
     __syncthreads();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int px = p1 - p0;
-    for (int g = warp; g < a.G; g += kBlock / 32) {
-        const Joined r = warp_join(a.lanes * a.cg, lane, [&](int i, float &c) {
-            const int l = i / a.cg;
-            c = static_cast<float>((px - l + a.lanes - 1) / a.lanes);  // pixels of lane l
-            return buf[l * a.C + g * a.cg + (i - l * a.cg)];
-        });
-        if (lane == 0)
+    const int w = join_width(a.G);
+    for (int g0 = 0; g0 < a.G; g0 += kBlock / w) {
+        const int g = g0 + threadIdx.x / w;
+        const Joined r = join_threads(buf + g * width, px, a.lanes, pitch, width, each, w, g < a.G);
+        if (g < a.G && threadIdx.x % w == 0)
             a.part[(static_cast<size_t>(b) * a.chunks + blockIdx.x) * a.G + g] =
                 make_float2(static_cast<float>(r.mean), static_cast<float>(r.m2));
     }
 }
 
-// One vector of V outputs of pixel p (of image b), channels c.. on.
+// One vector of V outputs of pixel p (of image b), channels c on.
 template <typename T, int V, int OUT>
-__device__ __forceinline__ void emit(const NormArgs &a, int b, int p, int c, float (&y)[V])
+__device__ __forceinline__ void emit(const NormArgs &a, int b, int p, int c, F2 (&f)[kPairs<V>])
 {
-    const size_t at = (static_cast<size_t>(b) * a.HW + p) * a.C + c;
-    if (OUT == kNormSame) {
-        Vec<T, V> v;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            v.e[i] = from_f<T>(y[i]);
-        store_vec<T, V>(static_cast<T *>(a.y) + at, v);
-    } else if (OUT == kNormI8) {
-        // NC/32HW32; saturating convert-to-integer, NaN to 0
-        Vec<int8_t, V> v;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            v.e[i] = static_cast<int8_t>(max(-128, min(127, __float2int_rn(y[i] * a.q_mul))));
-        int8_t *q = static_cast<int8_t *>(a.y) +
-                    ((static_cast<size_t>(b) * (a.C / 32) + c / 32) * a.HW + p) * 32 + c % 32;
-        store_vec<int8_t, V>(q, v);
+    const size_t row = static_cast<size_t>(b) * a.HW + p;
+    if constexpr (OUT == kNormSame) {
+        store_vec<T, V>(static_cast<T *>(a.y) + row * a.C + c, finish<T, V>(f, a.act));
     } else {
-        // The 32 / V neighbouring threads that hold a block agree on its scale
-        // (they belong to one pixel, so they are here together).
-        constexpr int L = 32 / V;
-        uint32_t m = 0;
+        float y[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-        const int lane = threadIdx.x & 31;
-        const uint32_t mask = ((L == 32 ? 0u : (1u << (L & 31))) - 1u) << (lane & ~(L - 1));
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 t = un2(f[i]);
+            y[2 * i] = t.x;
+            y[2 * i + 1] = t.y;
+        }
+        activate(y, a.act);
+        if constexpr (OUT == kNormI8) {
+            // NC/32HW32; rounded to an integer (NaN: 0), then packed with saturation
+            uint32_t w[V / 4];
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1)
-            m = max(m, __shfl_xor_sync(mask, m, o));
-        const uint32_t s = mx4_scale_byte(m);
-        const float inv = mx4_inverse_scale(min(s, 252u));
+            for (int i = 0; i < V / 4; ++i) {
+                int n[4];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            y[i] *= inv;
-        uint8_t *q = static_cast<uint8_t *>(a.y) + at / 2;
-        if constexpr (V == 8)
-            *reinterpret_cast<uint32_t *>(q) = s == 255u ? 0u : e2m1x8(y);
-        else if constexpr (V == 4)
-            *reinterpret_cast<uint16_t *>(q) = s == 255u ? uint16_t{0} : e2m1x4(y);
-        if ((lane & (L - 1)) == 0) {
-            const int kt = (a.C + 127) / 128, blk = c / 32;
-            uint8_t *d = a.sf + mx4_scale_at(static_cast<long long>(b) * a.HW + p, blk, kt);
-            *d = static_cast<uint8_t>(s);
-            if (blk == a.C / 32 - 1)  // the row's last block: the rest of its tile is padding
-                for (int k = 1; k < 4 - (blk & 3); ++k)
-                    d[k] = 0;
+                for (int j = 0; j < 4; ++j)
+                    n[j] = __float2int_rn(y[4 * i + j] * a.q_mul);
+                uint32_t hi;
+                asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
+                    : "=r"(hi)
+                    : "r"(n[3]), "r"(n[2]), "r"(0));
+                asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
+                    : "=r"(w[i])
+                    : "r"(n[1]), "r"(n[0]), "r"(hi));
+            }
+            int8_t *q = static_cast<int8_t *>(a.y) +
+                        ((static_cast<size_t>(b) * (a.C / 32) + c / 32) * a.HW + p) * 32 + c % 32;
+            if constexpr (V == 8)
+                *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint32_t *>(q) = w[0];
+        } else {
+            // The 32 / V neighbouring threads that hold a block agree on its scale
+            // (they belong to one pixel, so they are here together).
+            constexpr int L = 32 / V;
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+            const int lane = threadIdx.x & 31;
+            const uint32_t mask = ((1u << L) - 1u) << (lane & ~(L - 1));
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1)
+                m = max(m, __shfl_xor_sync(mask, m, o));
+            const uint32_t s = mx4_scale_byte(m);
+            const float inv = mx4_inverse_scale(min(s, 252u));
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                y[i] *= inv;
+            uint8_t *q = static_cast<uint8_t *>(a.y) + (row * a.C + c) / 2;
+            if constexpr (V == 8)
+                *reinterpret_cast<uint32_t *>(q) = s == 255u ? 0u : e2m1x8(y);
+            else
+                *reinterpret_cast<uint16_t *>(q) = s == 255u ? uint16_t{0} : e2m1x4(y);
+            if ((lane & (L - 1)) == 0) {
+                const int kt = (a.C + 127) / 128, blk = c / 32;
+                uint8_t *d = a.sf + mx4_scale_at(static_cast<long long>(row), blk, kt);
+                *d = static_cast<uint8_t>(s);
+                if (blk == a.C / 32 - 1)  // the row's last block: the rest of its tile is padding
+                    for (int k = 1; k < 4 - (blk & 3); ++k)
+                        d[k] = 0;
+            }
         }
     }
 }
@@ -298,210 +360,219 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
     extern __shared__ Coef coef[];  // [G]
     griddep_wait();
     const int b = a.b0 + blockIdx.y;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int g = warp; g < a.G; g += kBlock / 32) {
+    const int p0 = blockIdx.x * a.chunk, px = min(a.HW - p0, a.chunk);
+    // Join the chunks' statistics, in 64 bits.
+    const int w = join_width(a.G);
+    const double last = static_cast<double>(a.HW - (a.chunks - 1) * a.chunk) * a.cg;
+    const double whole = static_cast<double>(a.chunk) * a.cg;
+    for (int g0 = 0; g0 < a.G; g0 += kBlock / w) {
+        const int g = g0 + threadIdx.x / w, lane = threadIdx.x & (w - 1);
         const float2 *part = a.part + static_cast<size_t>(b) * a.chunks * a.G + g;
-        const Joined r = warp_join(a.chunks, lane, [&](int i, float &c) {
-            c = static_cast<float>(min(a.HW, (i + 1) * a.chunk) - i * a.chunk) * a.cg;
-            return part[static_cast<size_t>(i) * a.G];
-        });
-        if (lane == 0)
-            coef[g] = make_coef(r, static_cast<double>(a.HW) * a.cg, a.eps);
+        constexpr int kKeep = 8;  // parts a lane holds from the first pass to the second
+        float2 kept[kKeep];
+        double sum = 0., m2 = 0.;
+        const int mine = g < a.G && lane < a.chunks ? (a.chunks - lane + w - 1) / w : 0;
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (j < mine)
+                kept[j] = part[static_cast<size_t>(lane + j * w) * a.G];
+        const auto weight = [&](int j) { return lane + j * w == a.chunks - 1 ? last : whole; };
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (j < mine)
+                sum += weight(j) * kept[j].x;
+#pragma unroll 4
+        for (int j = kKeep; j < mine; ++j)
+            sum += weight(j) * part[static_cast<size_t>(lane + j * w) * a.G].x;
+        const double mean = lanes_sum(sum, w) / a.count;
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (j < mine)
+                m2 += kept[j].y + weight(j) * (kept[j].x - mean) * (kept[j].x - mean);
+#pragma unroll 4
+        for (int j = kKeep; j < mine; ++j) {
+            const float2 p = part[static_cast<size_t>(lane + j * w) * a.G];
+            m2 += p.y + weight(j) * (p.x - mean) * (p.x - mean);
+        }
+        m2 = lanes_sum(m2, w);
+        if (g < a.G && lane == 0)
+            coef[g] = make_coef(Joined{mean, m2}, a.count, a.eps);
     }
     if (OUT == kNormMx4 && b == 0 && blockIdx.x == 0)
         mx4_zero_row_padding(a.sf, static_cast<long long>(a.B) * a.HW, (a.C + 127) / 128,
                              threadIdx.x, kBlock);
     __syncthreads();
-    const int p0 = blockIdx.x * a.chunk, p1 = min(a.HW, p0 + a.chunk);
-    const size_t base = static_cast<size_t>(b) * a.HW * a.C;
     const int pl = threadIdx.x / a.nv;
-    if (pl >= a.lanes)
-        return;
-    for (int cv = threadIdx.x - pl * a.nv; cv < a.nv; cv += kBlock) {
-        const Affine<V> f(a, coef, 0, cv * V);
-        const T *x = static_cast<const T *>(a.x) + base + cv * V;
-        const T *r = a.r ? static_cast<const T *>(a.r) + base + cv * V : nullptr;
-        for (int p = p0 + pl; p < p1; p += kBatch * a.lanes) {
-            Vec<T, V> v[kBatch], w[kBatch];
+    const int mine = pl < a.lanes && px > pl ? (px - pl + a.lanes - 1) / a.lanes : 0;
+    const size_t step = static_cast<size_t>(a.lanes) * a.C;
+    for (int cv = threadIdx.x - pl * a.nv; cv < a.nv && mine > 0; cv += kBlock) {
+        const Affine<T, V> f(a, coef, cv * V, cv * V, a.cg % V == 0);
+        const size_t base = (static_cast<size_t>(b) * a.HW + p0 + pl) * a.C + cv * V;
+        const T *x = static_cast<const T *>(a.x) + base;
+        const T *r = a.r ? static_cast<const T *>(a.r) + base : nullptr;
+        for (int i0 = 0; i0 < mine; i0 += kBatch) {
+            Vec<T, V> v[kBatch], rv[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int q = p + j * a.lanes;
-                if (q < p1) {
-                    v[j] = load_vec<T, V>(x + static_cast<size_t>(q) * a.C);
+                if (i0 + j < mine) {
+                    v[j] = load_vec<T, V>(x + j * step);
                     if (r)
-                        w[j] = load_vec<T, V>(r + static_cast<size_t>(q) * a.C);
+                        rv[j] = load_vec<T, V>(r + j * step);
                 }
             }
+            x += kBatch * step;
+            if (r)
+                r += kBatch * step;
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int q = p + j * a.lanes;
-                if (q < p1) {
-                    float y[V];
-                    f.apply(a, v[j], r ? &w[j] : nullptr, y);
-                    emit<T, V, OUT>(a, b, q, cv * V, y);
+                if (i0 + j < mine) {
+                    F2 y[kPairs<V>];
+                    f.apply(v[j], r ? &rv[j] : nullptr, y);
+                    emit<T, V, OUT>(a, b, p0 + pl + (i0 + j) * a.lanes, cv * V, y);
                 }
             }
         }
     }
 }
 
-// The cluster form: CTA `rank` of the cluster (image b, channel slice sl) holds
-// the slice's channels of pixels [p0, p1).  A thread keeps its vectors in slots
-// of its own (slot i of thread t at (i * threads + t) * 16 bytes), so the data
-// itself needs no synchronisation.
+// The cluster form: CTA `rank` of the cluster (image b, channel slice) holds the
+// slice's channels of pixels p0 .. p0 + px - 1.  A thread keeps its vectors in
+// slots of its own (slot i of thread t at (i * threads + t)), so the data itself
+// needs no synchronisation.
 template <typename T, int V, int OUT>
 __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
 {
     extern __shared__ uint4 dyn[];
     using Slot = Vec<T, V>;
-    Slot *slots = reinterpret_cast<Slot *>(dyn);
-    // behind the slots: the joined statistics of this CTA, and the coefficients
-    const int groups = a.Cs / a.cg;
-    float2 *buf = reinterpret_cast<float2 *>(
-        reinterpret_cast<uint8_t *>(dyn) + static_cast<size_t>(a.iters) * kBlock * sizeof(Slot));
     const bool one = a.cg % V == 0;  // a vector lies within one group
-    const int per = one ? 1 : V;     // partial results of a thread
+    const int each = one ? V : 1, per = V / each;
+    const int groups = a.Cs / a.cg;
+    // slots of x (and of the shortcut), the threads' statistics, the CTA's, the coefficients
+    Slot *slots = reinterpret_cast<Slot *>(dyn) + threadIdx.x;
+    float2 *buf = reinterpret_cast<float2 *>(reinterpret_cast<Slot *>(dyn) +
+                                             (a.stage_r ? 2 : 1) * a.iters * kBlock);
     double2 *cta = reinterpret_cast<double2 *>(buf + kBlock * per);
     Coef *coef = reinterpret_cast<Coef *>(cta + groups);
     uint32_t ctas;
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
     const uint32_t rank = cluster_ctarank();
     const int unit = blockIdx.x / ctas, b = unit / a.slices;
-    const int c0 = (unit - b * a.slices) * a.Cs;
     const int share = (a.HW + ctas - 1) / ctas;
-    const int p0 = min(a.HW, static_cast<int>(rank) * share), p1 = min(a.HW, p0 + share);
+    const int p0 = static_cast<int>(rank) * share, px = max(0, min(a.HW - p0, share));
     const int pl = threadIdx.x / a.nv, cv = threadIdx.x - pl * a.nv;
-    const size_t base = static_cast<size_t>(b) * a.HW * a.C + c0 + cv * V;
-    const bool active = pl < a.lanes;
+    const int c = (unit - b * a.slices) * a.Cs + cv * V;
+    const int mine = pl < a.lanes && px > pl ? (px - pl + a.lanes - 1) / a.lanes : 0;
+    const size_t base = (static_cast<size_t>(b) * a.HW + p0 + pl) * a.C + c;
+    const size_t step = static_cast<size_t>(a.lanes) * a.C;
+    const T *r = a.r ? static_cast<const T *>(a.r) + base : nullptr;
 
     griddep_wait();
     if (OUT == kNormMx4 && blockIdx.x == 0)
         mx4_zero_row_padding(a.sf, static_cast<long long>(a.B) * a.HW, (a.C + 127) / 128,
                              threadIdx.x, kBlock);
-    // Load, keep, and sum about the first value.
-    float k[V], s[V], q[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        k[i] = s[i] = q[i] = 0.f;
-    const int mine = active && p0 + pl < p1 ? (p1 - p0 - pl + a.lanes - 1) / a.lanes : 0;
+    // Every copy of the thread is in flight before the first is used: x in two
+    // groups, so that the sums run behind the arrivals, then the shortcut.
+    const int half = (mine + 1) / 2;
     {
-        const T *x = static_cast<const T *>(a.x) + base + static_cast<size_t>(p0 + pl) * a.C;
-        const size_t step = static_cast<size_t>(a.lanes) * a.C;
-        for (int i0 = 0; i0 < mine; i0 += kBatch) {
-            Slot v[kBatch];
+        const T *x = static_cast<const T *>(a.x) + base;
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (i0 + j < mine)
-                    v[j] = load_vec<T, V>(x + (i0 + j) * step);
-            if (i0 == 0) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    k[i] = to_f(v[0].e[i]);
+        for (int h = 0; h < 2; ++h) {
+            const int end = h ? mine : half;
+            for (int i = h ? half : 0; i < end; ++i, x += step) {
+                if constexpr (sizeof(Slot) >= 4)
+                    copy_async<sizeof(Slot)>(slots + i * kBlock, x);
+                else
+                    slots[i * kBlock] = load_vec<T, V>(x);
             }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (i0 + j < mine) {
-                    slots[(i0 + j) * kBlock + threadIdx.x] = v[j];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float d = to_f(v[j].e[i]) - k[i];
-                        s[i] += d;
-                        q[i] = fmaf(d, d, q[i]);
-                    }
-                }
+            copy_commit();
+        }
+        if (a.stage_r) {
+            const T *rr = r;
+            for (int i = 0; i < mine; ++i, rr += step) {
+                if constexpr (sizeof(Slot) >= 4)
+                    copy_async<sizeof(Slot)>(slots + (a.iters + i) * kBlock, rr);
+                else
+                    slots[(a.iters + i) * kBlock] = load_vec<T, V>(rr);
             }
         }
+        copy_commit();
     }
-    // (mean, M2) of each channel, or of the thread's whole vector
     {
-        const float inv = mine ? 1.f / static_cast<float>(mine) : 0.f;
-        float mean = 0.f, m2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float ms = s[i] * inv;
-            k[i] += ms;
-            q[i] = fmaxf(fmaf(-ms, s[i], q[i]), 0.f);
-            mean += k[i] - k[0];
+        Sums<V> st;
+        copy_wait<2>();
+        if (mine > 0) {
+            st.start(slots[0]);
+            for (int i = 1; i < half; ++i)
+                st.add(slots[i * kBlock]);
         }
-        if (one) {
-            mean = k[0] + mean * (1.f / V);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = k[i] - mean;
-                m2 += fmaf(d * d, static_cast<float>(mine), q[i]);
-            }
-            buf[threadIdx.x] = make_float2(mean, m2);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                buf[threadIdx.x * V + i] = make_float2(k[i], q[i]);
+        copy_wait<1>();
+        if (mine > 0) {
+            for (int i = half; i < mine; ++i)
+                st.add(slots[i * kBlock]);
+            st.write(mine, one, buf + threadIdx.x * per);
         }
     }
     __syncthreads();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int px = p1 - p0;
-    const int width = one ? a.cg / V : a.cg, pitch = one ? a.nv : a.Cs;
-    for (int g = warp; g < groups; g += kBlock / 32) {
-        const Joined r = warp_join(a.lanes * width, lane, [&](int i, float &c) {
-            const int l = i / width;
-            c = px > l ? static_cast<float>((px - l + a.lanes - 1) / a.lanes * (one ? V : 1)) : 0.f;
-            return c > 0.f ? buf[l * pitch + g * width + (i - l * width)] : make_float2(0.f, 0.f);
-        });
-        if (lane == 0) {
-            if (ctas == 1)
-                coef[g] = make_coef(r, static_cast<double>(a.HW) * a.cg, a.eps);
-            else
-                cta[g] = make_double2(px > 0 ? r.mean : 0., px > 0 ? r.m2 : 0.);
+    {
+        const int w = join_width(groups), width = a.cg / each, pitch = a.Cs / each;
+        for (int g0 = 0; g0 < groups; g0 += kBlock / w) {
+            const int g = g0 + threadIdx.x / w;
+            const Joined t = join_threads(buf + g * width, px, a.lanes, pitch, width, each, w,
+                                          g < groups && px > 0);
+            if (g < groups && threadIdx.x % w == 0) {
+                if (ctas == 1)
+                    coef[g] = make_coef(t, a.count, a.eps);
+                else
+                    cta[g] = px > 0 ? make_double2(t.mean, t.m2) : make_double2(0., 0.);
+            }
         }
     }
     if (ctas > 1) {
         cluster_sync_all();
-        for (int g = threadIdx.x; g < groups; g += kBlock) {
-            // every CTA joins the same parts in the same order
-            const uint32_t at = smem_u32(cta + g);
-            const double total = static_cast<double>(a.HW) * a.cg;
-            double mean = 0., m2 = 0.;
-            for (int pass = 0; pass < 2; ++pass) {
-                for (uint32_t r = 0; r < ctas; ++r) {
-                    double m, v;
-                    asm volatile("ld.shared::cluster.v2.f64 {%0, %1}, [%2];"
-                                 : "=d"(m), "=d"(v)
-                                 : "r"(mapa_shared(at, r))
-                                 : "memory");
-                    const int q0 = min(a.HW, static_cast<int>(r) * share);
-                    const double n = static_cast<double>(min(a.HW, q0 + share) - q0) * a.cg;
-                    if (pass == 0)
-                        mean += n * m;
-                    else if (n > 0.)
-                        m2 += v + n * (m - mean) * (m - mean);
-                }
-                if (pass == 0)
-                    mean /= total;
+        // Every CTA joins the same parts in the same order: a lane per CTA.
+        for (int g0 = 0; g0 < groups; g0 += kBlock / 8) {
+            const int g = g0 + threadIdx.x / 8, q = threadIdx.x & 7;
+            double m = 0., v = 0., n = 0.;
+            if (g < groups && q < static_cast<int>(ctas)) {
+                asm volatile("ld.shared::cluster.v2.f64 {%0, %1}, [%2];"
+                             : "=d"(m), "=d"(v)
+                             : "r"(mapa_shared(smem_u32(cta + g), q))
+                             : "memory");
+                n = static_cast<double>(max(0, min(a.HW - q * share, share))) * a.cg;
             }
-            coef[g] = make_coef(Joined{mean, m2}, total, a.eps);
+            const double mean = lanes_sum(n * m, 8) / a.count;
+            const double m2 = lanes_sum(n > 0. ? v + n * (m - mean) * (m - mean) : 0., 8);
+            if (g < groups && q == 0)
+                coef[g] = make_coef(Joined{mean, m2}, a.count, a.eps);
         }
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
+    copy_wait<0>();
     __syncthreads();
-    if (active) {
-        const Affine<V> f(a, coef, c0, cv * V);
-        const T *r = a.r ? static_cast<const T *>(a.r) + base + static_cast<size_t>(p0 + pl) * a.C
-                         : nullptr;
-        const size_t step = static_cast<size_t>(a.lanes) * a.C;
-        for (int i0 = 0; i0 < mine; i0 += kBatch) {
-            Slot w[kBatch];
-            if (r) {
+    if (mine > 0) {
+        const Affine<T, V> f(a, coef, c, cv * V, one);
+        if (a.stage_r || !r) {
+            const int second = r ? a.iters * kBlock : 0;
+#pragma unroll 2
+            for (int i = 0; i < mine; ++i) {
+                F2 y[kPairs<V>];
+                f.apply(slots[i * kBlock], r ? &slots[second + i * kBlock] : nullptr, y);
+                emit<T, V, OUT>(a, b, p0 + pl + i * a.lanes, c, y);
+            }
+        } else {
+            for (int i0 = 0; i0 < mine; i0 += kBatch, r += kBatch * step) {
+                Slot rv[kBatch];
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j)
                     if (i0 + j < mine)
-                        w[j] = load_vec<T, V>(r + (i0 + j) * step);
-            }
+                        rv[j] = load_vec<T, V>(r + j * step);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (i0 + j < mine) {
-                    float y[V];
-                    f.apply(a, slots[(i0 + j) * kBlock + threadIdx.x], r ? &w[j] : nullptr, y);
-                    emit<T, V, OUT>(a, b, p0 + pl + (i0 + j) * a.lanes, c0 + cv * V, y);
+                for (int j = 0; j < kBatch; ++j) {
+                    if (i0 + j < mine) {
+                        F2 y[kPairs<V>];
+                        f.apply(slots[(i0 + j) * kBlock], &rv[j], y);
+                        emit<T, V, OUT>(a, b, p0 + pl + (i0 + j) * a.lanes, c, y);
+                    }
                 }
             }
         }
@@ -527,18 +598,21 @@ struct Plan {
     int V, nv, lanes;
     int chunks, chunk;                    // two-launch form
     int cluster, Cs, slices, iters, smem;  // cluster form (cluster = 0: two launches)
+    int stage_r;
 };
 
-double norm_cost(double ctas, double smem, int segment, int cluster, int iters)
+constexpr long long kSmemMost = 220 * 1024;
+
+double norm_cost(double ctas, double smem, int segment, int cluster, bool direct_r)
 {
     // resident CTAs per SM by shared memory and threads
     const double fit = std::min(3.0, std::floor(227.0 * 1024 / (smem + 1024)));
     double t = std::ceil(ctas / (148 * fit)) * fit * (smem + 3000);  // bytes an SM handles
     t *= 1 + 0.15 * (3 - fit) + (segment < 128 ? 0.1 : 0.0) + (segment < 64 ? 0.4 : 0.0);
-    return t + 2000 * (cluster > 1) + 500 * cluster;
+    return t * (direct_r ? 1.5 : 1.) + 2000 * (cluster > 1) + 500 * cluster;
 }
 
-Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks)
+Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool res)
 {
     Plan p{};
     const int elt = dtype == X1CB_F32 ? 4 : 2, cg = C / G;
@@ -563,12 +637,16 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks)
             if (iters > kFold)
                 continue;
             const int groups = Cs / cg;
-            const long long smem = static_cast<long long>(iters) * kBlock * p.V * elt +
-                                   kBlock * (cg % p.V ? p.V : 1) * 8 + groups * (16 + 12);
-            if (smem > 220 * 1024)
+            const long long data = static_cast<long long>(iters) * kBlock * p.V * elt;
+            const long long rest = kBlock * (cg % p.V ? p.V : 1) * 8 + groups * (16 + 12);
+            if (data + rest > kSmemMost)
                 continue;
+            const bool stage_r = res && 2 * data + rest <= kSmemMost;
+            const long long smem = rest + (stage_r ? 2 : 1) * data;
             const double ctas = static_cast<double>(B) * (C / Cs) * k;
-            const double cost = norm_cost(ctas, smem, Cs * elt, k, iters);
+            if (ctas > INT_MAX)
+                continue;
+            const double cost = norm_cost(ctas, smem, Cs * elt, k, res && !stage_r);
             if (cost < best) {
                 best = cost;
                 p.cluster = k;
@@ -578,19 +656,19 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks)
                 p.lanes = lanes;
                 p.iters = iters;
                 p.smem = static_cast<int>(smem);
+                p.stage_r = stage_r;
             }
         }
     }
-    if (p.cluster && static_cast<long long>(B) * p.slices * p.cluster <= INT_MAX)
+    if (p.cluster)
         return p;
-    p.cluster = 0;
     p.nv = C / p.V;
     p.lanes = std::max(1, kBlock / p.nv);
     // four blocks per SM at once, at least two batches a thread
     const long long want = std::max(1, 148 * 4 / B);
     const long long most = std::max(1, HW / (p.lanes * kBatch * 2));
     p.chunks = static_cast<int>(std::min(want, most));
-    p.chunk = (HW + p.chunks - 1) / p.chunks;
+    p.chunk = std::min((HW + p.chunks - 1) / p.chunks, kFold * p.lanes);
     p.chunks = (HW + p.chunk - 1) / p.chunk;
     return p;
 }
@@ -694,7 +772,7 @@ size_t norm_workspace_floats(int dtype, int B, int HW, int C, int G)
 {
     size_t n = 0;
     for (int whole = 0; whole <= (C % 32 == 0 ? 1 : 0); ++whole) {
-        const Plan p = plan_norm(dtype, B, HW, C, G, whole != 0);
+        const Plan p = plan_norm(dtype, B, HW, C, G, whole != 0, false);
         if (!p.cluster)
             n = std::max(n, static_cast<size_t>(B) * p.chunks * G * 2);
     }
@@ -703,7 +781,7 @@ size_t norm_workspace_floats(int dtype, int B, int HW, int C, int G)
 
 int launch_norm(const NormCall &c, cudaStream_t s)
 {
-    const Plan p = plan_norm(c.dtype, c.B, c.HW, c.C, c.G, c.out != kNormSame);
+    const Plan p = plan_norm(c.dtype, c.B, c.HW, c.C, c.G, c.out != kNormSame, c.r != nullptr);
     NormArgs a{};
     a.x = c.x;
     a.r = c.r;
@@ -727,6 +805,8 @@ int launch_norm(const NormCall &c, cudaStream_t s)
     a.Cs = p.Cs;
     a.slices = p.slices;
     a.iters = p.iters;
+    a.stage_r = p.stage_r;
+    a.count = static_cast<double>(c.HW) * a.cg;
     if (c.dtype == X1CB_F32)
         return run_v<float>(c, p, a, s);
     return c.dtype == X1CB_BF16 ? run_v<__nv_bfloat16>(c, p, a, s) : run_v<__half>(c, p, a, s);
