@@ -52,8 +52,15 @@ struct NormArgs {
     int Cs, slices;     // channels per slice, slices (cluster form)
     int iters;          // pixels per thread (cluster form)
     int stage_r;        // the shortcut goes through shared memory too
-    double count;       // values per group and image: HW * cg
+    double inv_count;   // 1 / (HW * cg), the values of a group of an image
+    uint32_t div_nv, div_lanes;  // ceil(2^32 / nv), ceil(2^32 / lanes), see quotient()
 };
+
+// n / d for n * d < 2^32, from m = ceil(2^32 / d) (d > 1; d = 1 is stored as 0).
+__device__ __forceinline__ int quotient(int n, uint32_t m)
+{
+    return m ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), m)) : n;
+}
 
 // Shifted sums of a thread's V channels over n pixels.
 template <int V> struct Sums {
@@ -125,26 +132,27 @@ struct Joined {
 
 // Joins the (mean, M2) that a block's threads wrote for one group: entry v of
 // pixel lane l at buf[l * pitch + v], v < width, each standing for n * each
-// values, n = px / lanes (+ 1 for the first px % lanes lanes).  The w lanes that
-// share the group take the pixel lanes in turn; whole warps call it.
-__device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int lanes, int pitch,
-                                               int width, int each, int w, bool active)
+// values, n = base (+ 1 for the first `more` lanes).  The w lanes that share the
+// group take the pixel lanes in turn; whole warps call it.
+__device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int base, int more,
+                                               int lanes, int pitch, int width, int each, int w,
+                                               bool active)
 {
     float s1 = 0.f, s2 = 0.f, ref = 0.f;
     if (active) {
         ref = buf[0].x;
-        const int base = px / lanes, more = px - base * lanes;
-        for (int l = threadIdx.x & (w - 1); l < lanes; l += w) {
+        const int filled = base ? lanes : more;  // lanes with pixels
+        for (int l = threadIdx.x & (w - 1); l < filled; l += w) {
             const float n = static_cast<float>((base + (l < more)) * each);
-            if (n == 0.f)
-                break;
             float t = 0.f, u = 0.f, m = 0.f;
             const float2 *p = buf + l * pitch;
+#pragma unroll 2
             for (int v = 0; v < width; ++v) {
-                const float d = p[v].x - ref;
+                const float2 e = p[v];
+                const float d = e.x - ref;
                 t += d;
                 u = fmaf(d, d, u);
-                m += p[v].y;
+                m += e.y;
             }
             s1 = fmaf(n, t, s1);
             s2 += fmaf(n, u, m);
@@ -152,8 +160,8 @@ __device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int la
     }
     s1 = lanes_sum(s1, w);
     s2 = lanes_sum(s2, w);
-    const double mean = s1 / (static_cast<double>(px) * (width * each));
-    return Joined{ref + mean, s2 - s1 * mean};
+    const float off = __fdividef(s1, static_cast<float>(px) * static_cast<float>(width * each));
+    return Joined{static_cast<double>(ref) + off, fmaxf(fmaf(-s1, off, s2), 0.f)};
 }
 
 // Lanes per group so that a block's threads cover all groups at once where they can.
@@ -169,19 +177,19 @@ __device__ __forceinline__ int join_width(int groups)
 struct Coef {
     float mu, mu_low, rstd;  // the mean as a float and that float's rounding error
 };
-__device__ __forceinline__ Coef make_coef(const Joined &j, double count, float eps)
+__device__ __forceinline__ Coef make_coef(const Joined &j, double inv_count, float eps)
 {
     Coef c;
     c.mu = static_cast<float>(j.mean);
     c.mu_low = static_cast<float>(j.mean - c.mu);
     // 1/sqrt(v): a 32-bit estimate and one Newton step in 64 bits
-    const double v = fmax(j.m2, 0.) / count + eps;
-    const double r = 1.f / sqrtf(static_cast<float>(v));
-    c.rstd = static_cast<float>(r * (1.5 - 0.5 * v * r * r));
-    if (!(v >= 1e-30))
-        c.rstd = static_cast<float>(1. / sqrt(v));  // (also infinity, NaN)
-    else if (v > 1e30)
-        c.rstd = static_cast<float>(1. / sqrt(v));
+    const double v = j.m2 * inv_count + eps;
+    double r = rsqrtf(static_cast<float>(v));
+    if (v > 1e-30 && v < 1e30)
+        r = r * (1.5 - 0.5 * v * r * r);
+    else
+        r = 1. / sqrt(v);
+    c.rstd = static_cast<float>(r);
     return c;
 }
 
@@ -207,8 +215,7 @@ template <typename T, int V> struct Affine {
             s[i] = a.gamma ? k.rstd * a.gamma[c + i] : k.rstd;
             const float beta = a.beta ? a.beta[c + i] : 0.f;
             m[i] = -k.mu;
-            b[i] = kSub ? fmaf(-k.mu_low, s[i], beta)
-                        : static_cast<float>(beta - (static_cast<double>(k.mu) + k.mu_low) * s[i]);
+            b[i] = fmaf(-k.mu_low, s[i], kSub ? beta : fmaf(-k.mu, s[i], beta));
         }
 #pragma unroll
         for (int i = 0; i < kPairs<V>; ++i) {
@@ -244,9 +251,10 @@ template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stat
     const int p0 = blockIdx.x * a.chunk, px = min(a.HW - p0, a.chunk);
     const bool one = a.cg % V == 0;
     const int each = one ? V : 1, width = a.cg / each, pitch = a.C / each;
-    const int pl = threadIdx.x / a.nv;
+    const int pl = quotient(threadIdx.x, a.div_nv);
+    const int per_lane = quotient(px, a.div_lanes), more = px - per_lane * a.lanes;
     if (pl < a.lanes) {
-        const int mine = px > pl ? (px - pl + a.lanes - 1) / a.lanes : 0;
+        const int mine = per_lane + (pl < more);
         const size_t step = static_cast<size_t>(a.lanes) * a.C;
         for (int cv = threadIdx.x - pl * a.nv; cv < a.nv && mine > 0; cv += kBlock) {
             const T *x = static_cast<const T *>(a.x) +
@@ -273,86 +281,112 @@ template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stat
     const int w = join_width(a.G);
     for (int g0 = 0; g0 < a.G; g0 += kBlock / w) {
         const int g = g0 + threadIdx.x / w;
-        const Joined r = join_threads(buf + g * width, px, a.lanes, pitch, width, each, w, g < a.G);
+        const Joined r = join_threads(buf + g * width, px, per_lane, more, a.lanes, pitch,
+                                      width, each, w, g < a.G);
         if (g < a.G && threadIdx.x % w == 0)
             a.part[(static_cast<size_t>(b) * a.chunks + blockIdx.x) * a.G + g] =
                 make_float2(static_cast<float>(r.mean), static_cast<float>(r.m2));
     }
 }
 
-// One vector of V outputs of pixel p (of image b), channels c on.
-template <typename T, int V, int OUT>
-__device__ __forceinline__ void emit(const NormArgs &a, int b, int p, int c, F2 (&f)[kPairs<V>])
-{
-    const size_t row = static_cast<size_t>(b) * a.HW + p;
-    if constexpr (OUT == kNormSame) {
-        store_vec<T, V>(static_cast<T *>(a.y) + row * a.C + c, finish<T, V>(f, a.act));
-    } else {
-        float y[V];
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float2 t = un2(f[i]);
-            y[2 * i] = t.x;
-            y[2 * i + 1] = t.y;
-        }
-        activate(y, a.act);
-        if constexpr (OUT == kNormI8) {
-            // NC/32HW32; rounded to an integer (NaN: 0), then packed with saturation
-            uint32_t w[V / 4];
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                int n[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    n[j] = __float2int_rn(y[4 * i + j] * a.q_mul);
-                uint32_t hi;
-                asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
-                    : "=r"(hi)
-                    : "r"(n[3]), "r"(n[2]), "r"(0));
-                asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
-                    : "=r"(w[i])
-                    : "r"(n[1]), "r"(n[0]), "r"(hi));
-            }
-            int8_t *q = static_cast<int8_t *>(a.y) +
-                        ((static_cast<size_t>(b) * (a.C / 32) + c / 32) * a.HW + p) * 32 + c % 32;
-            if constexpr (V == 8)
-                *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
-            else
-                *reinterpret_cast<uint32_t *>(q) = w[0];
+// Where a thread's outputs go: channels c .. c + V - 1 of pixel p of image b,
+// and of every `lanes`-th pixel after it.
+template <typename T, int V, int OUT> struct Out {
+    uint8_t *to;       // the next output, code or int8
+    size_t step;       // bytes to the one after it
+    uint8_t *scales;   // MX4: the scale array from this block of channels on
+    uint32_t row, kt;  // MX4: the pixel, counted over the batch; scale tiles per row
+    int pad;           // MX4: bytes of padding behind the row's last block
+
+    __device__ __forceinline__ Out(const NormArgs &a, int b, int p, int c)
+    {
+        const size_t at = static_cast<size_t>(b) * a.HW + p;
+        to = static_cast<uint8_t *>(a.y);
+        if constexpr (OUT == kNormSame) {
+            to += (at * a.C + c) * sizeof(T);
+            step = static_cast<size_t>(a.lanes) * a.C * sizeof(T);
+        } else if constexpr (OUT == kNormI8) {
+            to += ((static_cast<size_t>(b) * (a.C / 32) + c / 32) * a.HW + p) * 32 + c % 32;
+            step = static_cast<size_t>(a.lanes) * 32;
         } else {
-            // The 32 / V neighbouring threads that hold a block agree on its scale
-            // (they belong to one pixel, so they are here together).
-            constexpr int L = 32 / V;
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-            const int lane = threadIdx.x & 31;
-            const uint32_t mask = ((1u << L) - 1u) << (lane & ~(L - 1));
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1)
-                m = max(m, __shfl_xor_sync(mask, m, o));
-            const uint32_t s = mx4_scale_byte(m);
-            const float inv = mx4_inverse_scale(min(s, 252u));
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                y[i] *= inv;
-            uint8_t *q = static_cast<uint8_t *>(a.y) + (row * a.C + c) / 2;
-            if constexpr (V == 8)
-                *reinterpret_cast<uint32_t *>(q) = s == 255u ? 0u : e2m1x8(y);
-            else
-                *reinterpret_cast<uint16_t *>(q) = s == 255u ? uint16_t{0} : e2m1x4(y);
-            if ((lane & (L - 1)) == 0) {
-                const int kt = (a.C + 127) / 128, blk = c / 32;
-                uint8_t *d = a.sf + mx4_scale_at(static_cast<long long>(row), blk, kt);
-                *d = static_cast<uint8_t>(s);
-                if (blk == a.C / 32 - 1)  // the row's last block: the rest of its tile is padding
-                    for (int k = 1; k < 4 - (blk & 3); ++k)
-                        d[k] = 0;
-            }
+            to += (at * a.C + c) / 2;
+            step = static_cast<size_t>(a.lanes) * (a.C / 2);
+            const int blk = c / 32;
+            kt = (a.C + 127) / 128;
+            scales = a.sf + static_cast<size_t>(blk >> 2) * 512 + (blk & 3);
+            row = static_cast<uint32_t>(at);
+            pad = blk == a.C / 32 - 1 ? 3 - (blk & 3) : 0;
         }
     }
-}
+    __device__ __forceinline__ void put(const NormArgs &a, const F2 (&f)[kPairs<V>])
+    {
+        if constexpr (OUT == kNormSame) {
+            store_vec<T, V>(reinterpret_cast<T *>(to), finish<T, V>(f, a.act));
+        } else {
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 t = un2(f[i]);
+                y[2 * i] = t.x;
+                y[2 * i + 1] = t.y;
+            }
+            activate(y, a.act);
+            if constexpr (OUT == kNormI8) {
+                // rounded to an integer (NaN: 0), then packed with saturation
+                uint32_t w[V / 4];
+#pragma unroll
+                for (int i = 0; i < V / 4; ++i) {
+                    int n[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        n[j] = __float2int_rn(y[4 * i + j] * a.q_mul);
+                    uint32_t hi;
+                    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
+                        : "=r"(hi)
+                        : "r"(n[3]), "r"(n[2]), "r"(0));
+                    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
+                        : "=r"(w[i])
+                        : "r"(n[1]), "r"(n[0]), "r"(hi));
+                }
+                if constexpr (V == 8)
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+                else
+                    *reinterpret_cast<uint32_t *>(to) = w[0];
+            } else {
+                // The 32 / V neighbouring threads that hold a block agree on its
+                // scale (they belong to one pixel, so they are here together).
+                constexpr int L = 32 / V;
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+                const int lane = threadIdx.x & 31;
+                const uint32_t mask = ((1u << L) - 1u) << (lane & ~(L - 1));
+#pragma unroll
+                for (int o = 1; o < L; o <<= 1)
+                    m = max(m, __shfl_xor_sync(mask, m, o));
+                const uint32_t s = mx4_scale_byte(m);
+                const float inv = mx4_inverse_scale(min(s, 252u));
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    y[i] *= inv;
+                if constexpr (V == 8)
+                    *reinterpret_cast<uint32_t *>(to) = s == 255u ? 0u : e2m1x8(y);
+                else
+                    *reinterpret_cast<uint16_t *>(to) = s == 255u ? uint16_t{0} : e2m1x4(y);
+                if ((lane & (L - 1)) == 0) {
+                    uint8_t *d = scales + static_cast<size_t>(row >> 7) * kt * 512 +
+                                 (row & 31) * 16 + ((row >> 5) & 3) * 4;
+                    *d = static_cast<uint8_t>(s);
+                    for (int k = 1; k <= pad; ++k)
+                        d[k] = 0;
+                }
+                row += a.lanes;
+            }
+        }
+        to += step;
+    }
+};
 
 template <typename T, int V, int OUT>
 __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
@@ -384,7 +418,7 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
 #pragma unroll 4
         for (int j = kKeep; j < mine; ++j)
             sum += weight(j) * part[static_cast<size_t>(lane + j * w) * a.G].x;
-        const double mean = lanes_sum(sum, w) / a.count;
+        const double mean = lanes_sum(sum, w) * a.inv_count;
 #pragma unroll
         for (int j = 0; j < kKeep; ++j)
             if (j < mine)
@@ -396,20 +430,22 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
         }
         m2 = lanes_sum(m2, w);
         if (g < a.G && lane == 0)
-            coef[g] = make_coef(Joined{mean, m2}, a.count, a.eps);
+            coef[g] = make_coef(Joined{mean, m2}, a.inv_count, a.eps);
     }
     if (OUT == kNormMx4 && b == 0 && blockIdx.x == 0)
         mx4_zero_row_padding(a.sf, static_cast<long long>(a.B) * a.HW, (a.C + 127) / 128,
                              threadIdx.x, kBlock);
     __syncthreads();
-    const int pl = threadIdx.x / a.nv;
-    const int mine = pl < a.lanes && px > pl ? (px - pl + a.lanes - 1) / a.lanes : 0;
+    const int pl = quotient(threadIdx.x, a.div_nv);
+    const int per_lane = quotient(px, a.div_lanes), more = px - per_lane * a.lanes;
+    const int mine = pl < a.lanes ? per_lane + (pl < more) : 0;
     const size_t step = static_cast<size_t>(a.lanes) * a.C;
     for (int cv = threadIdx.x - pl * a.nv; cv < a.nv && mine > 0; cv += kBlock) {
         const Affine<T, V> f(a, coef, cv * V, cv * V, a.cg % V == 0);
         const size_t base = (static_cast<size_t>(b) * a.HW + p0 + pl) * a.C + cv * V;
         const T *x = static_cast<const T *>(a.x) + base;
         const T *r = a.r ? static_cast<const T *>(a.r) + base : nullptr;
+        Out<T, V, OUT> out(a, b, p0 + pl, cv * V);
         for (int i0 = 0; i0 < mine; i0 += kBatch) {
             Vec<T, V> v[kBatch], rv[kBatch];
 #pragma unroll
@@ -428,7 +464,7 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
                 if (i0 + j < mine) {
                     F2 y[kPairs<V>];
                     f.apply(v[j], r ? &rv[j] : nullptr, y);
-                    emit<T, V, OUT>(a, b, p0 + pl + (i0 + j) * a.lanes, cv * V, y);
+                    out.put(a, y);
                 }
             }
         }
@@ -456,12 +492,15 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
     uint32_t ctas;
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
     const uint32_t rank = cluster_ctarank();
-    const int unit = blockIdx.x / ctas, b = unit / a.slices;
+    uint32_t unit;
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(unit));
+    const int b = unit / static_cast<uint32_t>(a.slices);
     const int share = (a.HW + ctas - 1) / ctas;
     const int p0 = static_cast<int>(rank) * share, px = max(0, min(a.HW - p0, share));
-    const int pl = threadIdx.x / a.nv, cv = threadIdx.x - pl * a.nv;
-    const int c = (unit - b * a.slices) * a.Cs + cv * V;
-    const int mine = pl < a.lanes && px > pl ? (px - pl + a.lanes - 1) / a.lanes : 0;
+    const int pl = quotient(threadIdx.x, a.div_nv), cv = threadIdx.x - pl * a.nv;
+    const int per_lane = quotient(px, a.div_lanes), more = px - per_lane * a.lanes;
+    const int c = (static_cast<int>(unit) - b * a.slices) * a.Cs + cv * V;
+    const int mine = pl < a.lanes ? per_lane + (pl < more) : 0;
     const size_t base = (static_cast<size_t>(b) * a.HW + p0 + pl) * a.C + c;
     const size_t step = static_cast<size_t>(a.lanes) * a.C;
     const T *r = a.r ? static_cast<const T *>(a.r) + base : nullptr;
@@ -517,11 +556,11 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
         const int w = join_width(groups), width = a.cg / each, pitch = a.Cs / each;
         for (int g0 = 0; g0 < groups; g0 += kBlock / w) {
             const int g = g0 + threadIdx.x / w;
-            const Joined t = join_threads(buf + g * width, px, a.lanes, pitch, width, each, w,
-                                          g < groups && px > 0);
+            const Joined t = join_threads(buf + g * width, px, per_lane, more, a.lanes, pitch,
+                                          width, each, w, g < groups && px > 0);
             if (g < groups && threadIdx.x % w == 0) {
                 if (ctas == 1)
-                    coef[g] = make_coef(t, a.count, a.eps);
+                    coef[g] = make_coef(t, a.inv_count, a.eps);
                 else
                     cta[g] = px > 0 ? make_double2(t.mean, t.m2) : make_double2(0., 0.);
             }
@@ -540,10 +579,10 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
                              : "memory");
                 n = static_cast<double>(max(0, min(a.HW - q * share, share))) * a.cg;
             }
-            const double mean = lanes_sum(n * m, 8) / a.count;
+            const double mean = lanes_sum(n * m, 8) * a.inv_count;
             const double m2 = lanes_sum(n > 0. ? v + n * (m - mean) * (m - mean) : 0., 8);
             if (g < groups && q == 0)
-                coef[g] = make_coef(Joined{mean, m2}, a.count, a.eps);
+                coef[g] = make_coef(Joined{mean, m2}, a.inv_count, a.eps);
         }
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
@@ -551,13 +590,14 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
     __syncthreads();
     if (mine > 0) {
         const Affine<T, V> f(a, coef, c, cv * V, one);
+        Out<T, V, OUT> out(a, b, p0 + pl, c);
         if (a.stage_r || !r) {
             const int second = r ? a.iters * kBlock : 0;
 #pragma unroll 2
             for (int i = 0; i < mine; ++i) {
                 F2 y[kPairs<V>];
                 f.apply(slots[i * kBlock], r ? &slots[second + i * kBlock] : nullptr, y);
-                emit<T, V, OUT>(a, b, p0 + pl + i * a.lanes, c, y);
+                out.put(a, y);
             }
         } else {
             for (int i0 = 0; i0 < mine; i0 += kBatch, r += kBatch * step) {
@@ -571,7 +611,7 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
                     if (i0 + j < mine) {
                         F2 y[kPairs<V>];
                         f.apply(slots[(i0 + j) * kBlock], &rv[j], y);
-                        emit<T, V, OUT>(a, b, p0 + pl + (i0 + j) * a.lanes, c, y);
+                        out.put(a, y);
                     }
                 }
             }
@@ -603,13 +643,23 @@ struct Plan {
 
 constexpr long long kSmemMost = 220 * 1024;
 
+// What a cluster-form plan costs, in us, from measurements on B200: a CTA's
+// fixed part of 1.7 us, 17.4 KB/us through an SM, three CTAs at most to an SM
+// (registers), and factors for what slows a plan otherwise.  28 x 28 x 512 of
+// 16 bits, batch 128: 64 channels (100 KB) per CTA 45.3 us, 128 channels over
+// clusters of two (100 KB) 50.2, of four (50 KB) 57.4, 128 channels in one CTA
+// (200 KB) 53.2; 56 x 56 x 256, batch 64: 64-byte rows over clusters of two 49.2,
+// of 128 bytes over four 52.0.
 double norm_cost(double ctas, double smem, int segment, int cluster, bool direct_r)
 {
-    // resident CTAs per SM by shared memory and threads
     const double fit = std::min(3.0, std::floor(227.0 * 1024 / (smem + 1024)));
-    double t = std::ceil(ctas / (148 * fit)) * fit * (smem + 3000);  // bytes an SM handles
-    t *= 1 + 0.15 * (3 - fit) + (segment < 128 ? 0.1 : 0.0) + (segment < 64 ? 0.4 : 0.0);
-    return t * (direct_r ? 1.5 : 1.) + 2000 * (cluster > 1) + 500 * cluster;
+    const double rounds = std::ceil(ctas / (148 * fit));
+    // (a shortcut that does not fit beside x is read with little in flight)
+    const double bytes = direct_r ? 2.5 * smem : smem;
+    double t = rounds * (1.7 + std::min(fit, std::ceil(ctas / 148)) * bytes / 17400.);
+    t *= cluster == 1 ? 1. : cluster == 2 ? 1.1 : cluster == 4 ? 1.18 : 1.22;
+    t *= segment < 32 ? 1.6 : segment < 64 ? 1.25 : 1.;
+    return t * (fit == 1 ? 1.2 : 1.);
 }
 
 Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool res)
@@ -664,8 +714,8 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool r
         return p;
     p.nv = C / p.V;
     p.lanes = std::max(1, kBlock / p.nv);
-    // four blocks per SM at once, at least two batches a thread
-    const long long want = std::max(1, 148 * 4 / B);
+    // three blocks per SM at once, at least two batches a thread
+    const long long want = std::max(1, 148 * 3 / B);
     const long long most = std::max(1, HW / (p.lanes * kBatch * 2));
     p.chunks = static_cast<int>(std::min(want, most));
     p.chunk = std::min((HW + p.chunks - 1) / p.chunks, kFold * p.lanes);
@@ -806,7 +856,9 @@ int launch_norm(const NormCall &c, cudaStream_t s)
     a.slices = p.slices;
     a.iters = p.iters;
     a.stage_r = p.stage_r;
-    a.count = static_cast<double>(c.HW) * a.cg;
+    a.inv_count = 1. / (static_cast<double>(c.HW) * a.cg);
+    a.div_nv = p.nv > 1 ? static_cast<uint32_t>(((1ull << 32) + p.nv - 1) / p.nv) : 0;
+    a.div_lanes = p.lanes > 1 ? static_cast<uint32_t>(((1ull << 32) + p.lanes - 1) / p.lanes) : 0;
     if (c.dtype == X1CB_F32)
         return run_v<float>(c, p, a, s);
     return c.dtype == X1CB_BF16 ? run_v<__nv_bfloat16>(c, p, a, s) : run_v<__half>(c, p, a, s);
