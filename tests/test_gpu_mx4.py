@@ -161,6 +161,9 @@ CONV = [  # B, H, W, Ic, Oc
     (40, 16, 16, 256, 392),
     (16, 32, 32, 512, 2048),
     (1, 129, 127, 32, 8),
+    (40, 16, 16, 608, 1000),  # many tiles, ragged in every direction
+    (30, 20, 20, 288, 517),   # the same with rows that no 16-byte copy lines up with
+    (51, 28, 28, 128, 512),
 ]
 
 
@@ -173,7 +176,8 @@ def test_conv(shape, dtype, act, bias, res):
 
 
 @pytest.mark.parametrize("shape", [(1, 1, 1, 4096, 256), (1, 7, 7, 4096, 512), (3, 16, 16, 4096, 384),
-                                   (9, 16, 16, 608, 1000)])
+                                   (9, 16, 16, 608, 1000), (40, 16, 16, 608, 1000),
+                                   (30, 20, 20, 2080, 517), (41, 16, 16, 4096, 512)])
 def test_conv_exact(shape):
     """Operands whose sums fit 24 bits whatever their order: the result has to
     be exact, so that one wrong scale or element shows."""
@@ -215,7 +219,7 @@ def test_conv_row_masks():
     assert (got[17][~bad[17]] == 0).all()
 
 
-@pytest.mark.parametrize("M,Oc", [(1, 100), (50, 136), (300, 200), (300, 7)])
+@pytest.mark.parametrize("M,Oc", [(1, 100), (50, 136), (300, 200), (300, 7), (19000, 264)])
 def test_conv_leaves_the_rest_alone(M, Oc):
     g = _gen(6)
     (x, xs), _ = _operand(M, 128, g)
@@ -245,7 +249,7 @@ def test_conv_empty_and_refused():
 
 
 @pytest.mark.parametrize("shape", [(1, 1, 1, 2048, 1000), (1, 6, 6, 1024, 512),
-                                   (3, 28, 28, 256, 384)])
+                                   (3, 28, 28, 256, 384), (40, 16, 16, 256, 512)])
 def test_conv_capture_and_streams(shape):
     B, H, W, Ic, Oc = shape
     g, M = _gen(12), B * H * W
@@ -274,7 +278,7 @@ def test_conv_capture_and_streams(shape):
     assert torch.equal(a, want) and torch.equal(b, want2)
 
 
-@pytest.mark.parametrize("shape", [(1, 20, 20, 512, 256)])
+@pytest.mark.parametrize("shape", [(1, 20, 20, 512, 256), (50, 20, 20, 512, 256)])
 def test_conv_bounded_wait(shape):
     """A wait that runs out is reported, and the next call works."""
     B, H, W, Ic, Oc = shape

@@ -1,21 +1,26 @@
 // The MX4 1x1 convolution on the tensor cores: out[M, N] = act(x[M, K] w[N, K]^T
 // + bias + r), tcgen05.mma kind::mxf4 with one e8m0 scale per 32 elements.
 //
-// Persistent CTAs, one per SM; a tile is 128 rows (pixels) x kBN channels.
+// Persistent CTAs, one per SM; a tile is 128 rows (pixels) x kBN channels, or
+// 256 x 256 for a pair of CTAs that share each MMA (each holds half of the rows
+// and half of the channels' weights).
 //   warp 0      loads K steps of 256: x and w rows of 128 bytes (TMA, 128-byte
 //               swizzle) and their scale tiles (512 bytes per 128 rows x 128 K,
 //               stored in the order TMEM wants them) into a ring of stages;
-//   warp 1      copies the scales to TMEM (tcgen05.cp) and issues the MMAs, four
-//               K = 64 steps a stage.  The scale columns belong to the stage, so
-//               they are free exactly when the stage is;
-//   warps 4-11  epilogue: two warps per TMEM lane quarter, half the channels
-//               each, from two accumulators in turn, so that it runs beside the
-//               next tile's MMAs.
+//   warp 1      (of rank 0) copies the scales to TMEM (tcgen05.cp) and issues the
+//               MMAs, four K = 64 steps a stage.  The scale columns belong to the
+//               stage, so they are free exactly when the stage is;
+//   warps 4-11  epilogue: two warps per TMEM lane quarter, from two accumulators
+//               in turn, so that it runs beside the next tile's MMAs.  The pair's
+//               two accumulators of 256 columns share 128 columns (TMEM has 512,
+//               and the scales need theirs): the shared half is drained first and
+//               the next tile starts when it is free.
 // Every wait is bounded: on a timeout the CTA raises an abort flag, records a
 // status bit, lets its copies and MMAs land and leaves.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -29,14 +34,15 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kMxThreads = 32 * (4 + kEpiWarps);
-constexpr int kStageK = 256;             // elements: 128 bytes of codes a row
-constexpr int kRowsBytes = 128 * 128;    // codes of 128 rows in a stage
-constexpr int kSfBytes = 1024;           // scales of 128 rows in a stage
+constexpr int kStageK = 256;           // elements: 128 bytes of codes a row
+constexpr int kRowsBytes = 128 * 128;  // codes of 128 rows in a stage
+constexpr int kSfBytes = 1024;         // scales of 128 rows in a stage
 constexpr int kTmem = 512;
+constexpr int kIoBox = 32 * 128;       // an epilogue warp's 32 rows x 128 bytes
+constexpr int kMaxIo = 4;              // such boxes per warp
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct MxArgs {
-    const uint8_t *xs, *ws;
     const float *bias;
     const void *r;
     void *out;
@@ -44,47 +50,116 @@ struct MxArgs {
     uint64_t wait_ns;
     long long M;
     int K, N, act, inject;
-    int stages, k_steps, kt;      // ring depth; K steps of 256; scale tiles per row block
-    int m_tiles, n_tiles;
+    int stages, k_steps, kt;  // ring depth; K steps of 256; scale tiles per row block
+    int tiles, n_tiles;
+    int io;                   // boxes per epilogue warp (TMA epilogue)
 };
 
-template <int BN> struct Shape {
-    static constexpr int kW = BN * 128;                       // weight codes of a stage
-    static constexpr int kWsf = (BN + 127) / 128 * kSfBytes;  // their scales
-    static constexpr int kStage = kRowsBytes + kW + kSfBytes + kWsf;
-    static constexpr int kSfCols = 8 + (BN + 127) / 128 * 8;  // TMEM columns a stage's scales take
+template <int BN, bool kPair> struct Shape {
+    static constexpr int kBlocks = (BN + 127) / 128;  // scale blocks of the channels
+    static constexpr int kWRows = kPair ? BN / 2 : BN;
+    static constexpr int kW = kWRows * 128;           // weight codes of a stage
+    static constexpr int kStage = kRowsBytes + kW + kSfBytes * (1 + kBlocks);
+    static constexpr int kSfCols = 8 + kBlocks * 8;   // TMEM columns a stage's scales take
+    static constexpr bool kShared = BN == 256;        // accumulators that share columns
+    static constexpr int kSecond = kShared ? 128 : BN;  // first column of accumulator 1
+    static constexpr int kSfBase = kSecond + BN;
 };
 
-// Tail of the dynamic shared memory behind the ring.
-constexpr int kPatch = 32 * 33 * 4;  // an epilogue warp's transposing patch
+// Tail of the dynamic shared memory behind the ring and the epilogue's boxes.
+constexpr int kPatch = 32 * 33 * 4;  // an epilogue warp's transposing patch (plain epilogue)
 struct Tail {
-    unsigned long long bars[2 * 16 + 2 * 2 + 2];
+    alignas(16) float bias[kEpiWarps][64];  // read four at a time
+    unsigned long long bars[2 * 8 + 2 * 2 + 3];
+    unsigned long long r_full[kEpiWarps][kMaxIo];
     uint32_t tmem;
     int abort_flag;
 };
 
-template <typename T, int BN>
+// The boxes of 32 rows x 128 bytes that an epilogue warp works through, in
+// order: the tiles of the CTA, per tile the halves of 128 channels (shared
+// accumulator columns first), per half the boxes of the warp's side.
+template <typename T, int BN, bool kPair> struct Boxes {
+    using S = Shape<BN, kPair>;
+    static constexpr int kCols = 128 / sizeof(T);
+    static constexpr int kHalves = S::kShared ? 2 : 1;
+    static constexpr int kHalf = BN / kHalves;
+    static constexpr int kPer = kHalf / kCols;  // boxes per half, both sides
+    int t, step, end, n_tiles, side, row_off;
+    int half, box, parity;
+
+    __device__ __forceinline__ Boxes(const MxArgs &a, int unit, int units, int side_, int row_off_)
+        : t(unit), step(units), end(a.tiles), n_tiles(a.n_tiles), side(side_), row_off(row_off_),
+          half(0), box(side_), parity(0)
+    {
+        if (box >= kPer)
+            t = end;  // a side without boxes
+    }
+    __device__ __forceinline__ bool done() const { return t >= end; }
+    __device__ __forceinline__ bool first_of_half() const { return box == side; }
+    __device__ __forceinline__ bool last_of_half() const { return box + 2 >= kPer; }
+    __device__ __forceinline__ bool last_of_tile() const
+    {
+        return half == kHalves - 1 && last_of_half();
+    }
+    // first column within the tile
+    __device__ __forceinline__ int col() const
+    {
+        const int h = S::kShared ? (half ^ parity ^ 1) : 0;  // accumulator 0: upper half first
+        return h * kHalf + box * kCols;
+    }
+    __device__ __forceinline__ int channel() const { return t % n_tiles * BN + col(); }
+    __device__ __forceinline__ long long row() const
+    {
+        return static_cast<long long>(t / n_tiles) * (kPair ? 256 : 128) + row_off;
+    }
+    __device__ __forceinline__ void next()
+    {
+        box += 2;
+        if (box < kPer)
+            return;
+        box = side;
+        if (++half == kHalves) {
+            half = 0;
+            t += step;
+            parity ^= 1;
+        }
+    }
+};
+
+// kIo: outputs (and the shortcut) move as 32 x 128-byte boxes by TMA, which
+// needs rows of a multiple of 16 bytes; otherwise the plain epilogue transposes
+// through shared memory and stores element by element.
+template <typename T, int BN, bool kPair, bool kIo>
 __global__ void __launch_bounds__(kMxThreads, 1)
     conv_mx4_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                    MxArgs a)
+                    const __grid_constant__ CUtensorMap tmXs,
+                    const __grid_constant__ CUtensorMap tmWs,
+                    const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmO,
+                    const MxArgs a)
 {
-    using S = Shape<BN>;
+    using S = Shape<BN, kPair>;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
-    float *patches = reinterpret_cast<float *>(smem + a.stages * S::kStage);
-    Tail *tail = reinterpret_cast<Tail *>(smem + a.stages * S::kStage + kEpiWarps * kPatch);
+    // the epilogue's boxes first: they keep the 1024-byte alignment of the swizzle
+    const int epi_bytes = kEpiWarps * (kIo ? a.io * kIoBox : kPatch);
+    const uint32_t ring = sbase + ((epi_bytes + 1023) & ~1023);
+    Tail *tail = reinterpret_cast<Tail *>(smem + (ring - sbase) + a.stages * S::kStage);
     const uint32_t bars = smem_u32(tail->bars);
     const auto full = [&](int s) { return bars + 8u * s; };
     const auto empty = [&](int s) { return bars + 8u * (a.stages + s); };
     const auto acc_full = [&](int b) { return bars + 8u * (2 * a.stages + b); };
     const auto acc_empty = [&](int b) { return bars + 8u * (2 * a.stages + 2 + b); };
     const uint32_t mma_done = bars + 8u * (2 * a.stages + 4), never = mma_done + 8u;
+    const uint32_t exit_bar = never + 8u;
     volatile int *abort_flag = &tail->abort_flag;
     const WaitCtl ctl{abort_flag, a.status, a.inject == 1 ? 4 * a.wait_ns : a.wait_ns};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tiles = a.m_tiles * a.n_tiles;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x;
+    const int units = kPair ? gridDim.x >> 1 : gridDim.x;
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -94,20 +169,35 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), kEpiWarps);
+            mbar_init(acc_empty(b), kEpiWarps * (kPair ? 2 : 1));
         }
+        for (int w = 0; w < kEpiWarps; ++w)
+            for (int b = 0; b < kMaxIo; ++b)
+                mbar_init(smem_u32(&tail->r_full[w][b]), 1);
         mbar_init(mma_done, 1);
         mbar_init(never, 1);
+        mbar_init(exit_bar, 1);
         fence_mbar_init();
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmXs);
+        tma_prefetch_desc(&tmWs);
+        if (kIo)
+            tma_prefetch_desc(&tmO);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&tail->tmem), kTmem);
-        tmem_relinquish();
+        if (kPair) {
+            tmem_alloc_pair(smem_u32(&tail->tmem), kTmem);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(&tail->tmem), kTmem);
+            tmem_relinquish();
+        }
         tc_fence_before();
     }
     __syncthreads();
+    if (kPair)  // both CTAs' barriers and TMEM exist before traffic crosses
+        cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = tail->tmem;
     griddep_wait();  // from here on global memory is touched
@@ -117,29 +207,39 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = unit; ok && t < a.tiles; t += units) {
                 const int mt = t / a.n_tiles, nt = t - mt * a.n_tiles;
                 const int n0 = nt * BN;
-                const uint8_t *xs = a.xs + static_cast<size_t>(mt) * a.kt * 512;
+                const int xblk = kPair ? 2 * mt + static_cast<int>(rank) : mt;
                 for (int k = 0; k < a.k_steps; ++k) {
                     if (!mbar_wait(empty(s), ph ^ 1u, ctl, kDevTimeoutProducer)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t st = sbase + s * S::kStage;
-                    const uint32_t sfb = min(2, a.kt - 2 * k) * 512u;  // one tile at an odd end
-                    int wblk = 0;  // blocks of 128 weight rows that exist
+                    const uint32_t st = ring + s * S::kStage, sf = st + kRowsBytes + S::kW;
+                    if constexpr (kPair) {
+                        // both CTAs' loads complete on rank 0's barrier
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(full(s), 2 * S::kStage);
+                        const uint32_t bar = mapa_shared(full(s), 0);
+                        tma2_load_2d(st, &tmX, bar, k * 128, xblk * 128);
+                        tma2_load_2d(st + kRowsBytes, &tmW, bar, k * 128,
+                                     n0 + static_cast<int>(rank) * S::kWRows);
+                        tma2_load_2d(sf, &tmXs, bar, 0, xblk * a.kt + 2 * k);
 #pragma unroll
-                    for (int j = 0; j < (BN + 127) / 128; ++j)
-                        wblk += n0 + 128 * j < a.N;
-                    mbar_arrive_expect_tx(full(s), kRowsBytes + S::kW + sfb * (1 + wblk));
-                    tma_load_2d(st, &tmX, full(s), k * 128, mt * 128);
-                    tma_load_2d(st + kRowsBytes, &tmW, full(s), k * 128, n0);
-                    bulk_load(st + kRowsBytes + S::kW, xs + k * 1024, sfb, full(s));
-                    for (int j = 0; j < wblk; ++j)
-                        bulk_load(st + kRowsBytes + S::kW + kSfBytes * (1 + j),
-                                  a.ws + (static_cast<size_t>(n0 / 128 + j) * a.kt + 2 * k) * 512,
-                                  sfb, full(s));
+                        for (int j = 0; j < S::kBlocks; ++j)
+                            tma2_load_2d(sf + kSfBytes * (1 + j), &tmWs, bar, 0,
+                                         (n0 / 128 + j) * a.kt + 2 * k);
+                    } else {
+                        mbar_arrive_expect_tx(full(s), S::kStage);
+                        tma_load_2d(st, &tmX, full(s), k * 128, xblk * 128);
+                        tma_load_2d(st + kRowsBytes, &tmW, full(s), k * 128, n0);
+                        tma_load_2d(sf, &tmXs, full(s), 0, xblk * a.kt + 2 * k);
+#pragma unroll
+                        for (int j = 0; j < S::kBlocks; ++j)
+                            tma_load_2d(sf + kSfBytes * (1 + j), &tmWs, full(s), 0,
+                                        (n0 / 128 + j) * a.kt + 2 * k);
+                    }
                     ++issued;
                     if (++s == a.stages) {
                         s = 0;
@@ -148,51 +248,65 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 }
             }
             // Let every copy still in flight land (after a failed wait elsewhere
-            // nobody else waited for the last ones).
-            for (int i = max(0, issued - a.stages); i < issued; ++i)
-                if (!mbar_drain(full(i % a.stages), (i / a.stages) & 1, kDrainNs))
-                    atomicOr(a.status, kDevDrainFailed);
+            // nobody else waited for the last ones).  Of a pair, rank 0 waits for
+            // both and the exit handshake holds rank 1 until then.
+            if (rank == 0)
+                for (int i = max(0, issued - a.stages); i < issued; ++i)
+                    if (!mbar_drain(full(i % a.stages), (i / a.stages) & 1, kDrainNs))
+                        atomicOr(a.status, kDevDrainFailed);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         bool ok = true;
         if (a.inject == 1) {
             const WaitCtl planted{abort_flag, a.status, a.wait_ns};
             ok = __all_sync(0xffffffffu, mbar_wait(never, 0, planted, kDevTimeoutMma));
         }
-        int s = 0, buf = 0;
-        uint32_t ph = 0, aph = 0;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_empty(buf), aph ^ 1u, ctl, kDevTimeoutMma))) {
-                ok = false;
+        const auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, kPair ? mbar_wait_cl(bar, parity, ctl, kDevTimeoutMma)
+                                                 : mbar_wait(bar, parity, ctl, kDevTimeoutMma));
+        };
+        const auto commit = [&](uint32_t bar) {
+            if (kPair)
+                mma_commit_pair(bar);
+            else
+                mma_commit(bar);
+        };
+        int s = 0, i = 0;
+        uint32_t ph = 0;
+        for (int t = unit; ok && t < a.tiles; t += units, ++i) {
+            // The accumulator is free: its own last tile is drained, or with shared
+            // columns the tile before this one has left them.
+            if (S::kShared ? i > 0 && !wait(acc_empty(0), (i - 1) & 1)
+                           : !wait(acc_empty(i & 1), ((i >> 1) & 1) ^ 1))
                 break;
-            }
-            const uint32_t d = tmem + buf * BN;
+            tc_fence_after();
+            const uint32_t d = tmem + (i & 1) * S::kSecond;
             // BN = 64: the tile's scales are the lower or upper half of a 128-row block
             const uint32_t half = BN == 64 ? ((t % a.n_tiles) & 1) * 2u : 0u;
             for (int k = 0; k < a.k_steps; ++k) {
-                if (!__all_sync(0xffffffffu, mbar_wait(full(s), ph, ctl, kDevTimeoutMma))) {
+                if (!wait(full(s), ph)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = sbase + s * S::kStage;
-                const uint32_t sfa = tmem + 2 * BN + s * S::kSfCols, sfw = sfa + 8;
+                const uint32_t st = ring + s * S::kStage, sf = st + kRowsBytes + S::kW;
+                const uint32_t sfa = tmem + S::kSfBase + s * S::kSfCols, sfw = sfa + 8;
                 const int left = min(4, (a.K - k * kStageK + 63) / 64);
                 for (int j = 0; j < (left + 1) / 2; ++j) {
-                    tmem_cp_scales(sfa + 4 * j, smem_desc_scales(st + kRowsBytes + S::kW + 512 * j));
+                    tmem_cp_scales<kPair>(sfa + 4 * j, smem_desc_scales(sf + 512 * j));
 #pragma unroll
-                    for (int i = 0; i < (BN + 127) / 128; ++i)
-                        tmem_cp_scales(sfw + (BN + 127) / 128 * 4 * j + 4 * i,
-                                       smem_desc_scales(st + kRowsBytes + S::kW +
-                                                        kSfBytes * (1 + i) + 512 * j));
+                    for (int b = 0; b < S::kBlocks; ++b)
+                        tmem_cp_scales<kPair>(sfw + S::kBlocks * 4 * j + 4 * b,
+                                              smem_desc_scales(sf + kSfBytes * (1 + b) + 512 * j));
                 }
                 const uint64_t ad = smem_desc_sw128(st), bd = smem_desc_sw128(st + kRowsBytes);
                 for (int j = 0; j < left; ++j)
-                    mma_mx4(d, ad + 2 * j, bd + 2 * j, idesc_mx4(128, BN, (j & 1) * 2),
-                            sfa + 4 * (j >> 1), sfw + (BN + 127) / 128 * 4 * (j >> 1) + half,
-                            k > 0 || j > 0);
-                mma_commit(empty(s));
+                    mma_mx4<kPair>(d, ad + 2 * j, bd + 2 * j,
+                                   idesc_mx4(kPair ? 256 : 128, BN, (j & 1) * 2),
+                                   sfa + 4 * (j >> 1), sfw + S::kBlocks * 4 * (j >> 1) + half,
+                                   k > 0 || j > 0);
+                commit(empty(s));
                 if (++s == a.stages) {
                     s = 0;
                     ph ^= 1u;
@@ -200,74 +314,242 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
             if (!ok)
                 break;
-            mma_commit(acc_full(buf));
-            buf ^= 1;
-            aph ^= buf == 0;
+            commit(acc_full(i & 1));
         }
         // No MMA may still read shared memory or write TMEM behind this point.
-        mma_commit(mma_done);
+        commit(mma_done);
         if (lane == 0 && !mbar_drain(mma_done, 0, kDrainNs))
             atomicOr(a.status, kDevDrainFailed);
         __syncwarp();
     } else if (warp >= 4) {
         const int e = warp - 4, quarter = e & 3, side = e >> 2;
-        float *patch = patches + e * (kPatch / 4);
-        int buf = 0;
-        uint32_t aph = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-            const int mt = t / a.n_tiles, nt = t - mt * a.n_tiles;
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_full(buf), aph, ctl, kDevTimeoutEpilogue)))
-                break;
-            tc_fence_after();
-            const long long row0 = static_cast<long long>(mt) * 128 + quarter * 32;
-            const int rows = static_cast<int>(min(32ll, a.M - row0));
-            for (int c0 = side * (BN / 2); c0 < (side + 1) * (BN / 2); c0 += 32) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32_sync(tmem + buf * BN + c0 +
-                                            (static_cast<uint32_t>(quarter * 32) << 16),
-                                        v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    patch[lane * 33 + i] = __uint_as_float(v[i]);
-                __syncwarp();
-                const int o = nt * BN + c0 + lane;
-                if (o < a.N) {
-                    const float b = a.bias ? a.bias[o] : 0.f;
-                    size_t at = static_cast<size_t>(row0) * a.N + o;
-                    for (int i = 0; i < rows; ++i, at += a.N) {
-                        float y = patch[i * 33 + lane] + b;
-                        if (a.r)
-                            y += to_f(static_cast<const T *>(a.r)[at]);
-                        static_cast<T *>(a.out)[at] = from_f<T>(activate(y, a.act));
+        const uint32_t lanes_at = static_cast<uint32_t>(quarter * 32) << 16;
+        const int row_off = static_cast<int>(rank) * 128 + quarter * 32;
+        const auto release = [&](int b) {  // after the warp's reads of an accumulator
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair)
+                    mbar_arrive_cluster(mapa_shared(acc_empty(b), 0));
+                else
+                    mbar_arrive(acc_empty(b));
+            }
+        };
+        if constexpr (kIo) {
+            using B = Boxes<T, BN, kPair>;
+            const uint32_t boxes = sbase + e * a.io * kIoBox;
+            uint8_t *boxes_p = smem + e * a.io * kIoBox;
+            float *bias = tail->bias[e];
+            const uint32_t r_full = smem_u32(tail->r_full[e]);
+            B cur(a, unit, units, side, row_off), ahead = cur;
+            int n_ahead = 0;  // shortcut boxes asked for so far
+            const auto ask = [&](int most) {
+                // ask for shortcut boxes up to (not including) number `most`
+                for (; n_ahead < most && !ahead.done(); ++n_ahead, ahead.next()) {
+                    if (lane == 0 && ahead.row() < a.M && ahead.channel() < a.N) {
+                        const int d = n_ahead % a.io;
+                        mbar_arrive_expect_tx(r_full + 8 * d, kIoBox);
+                        tma_load_2d(boxes + d * kIoBox, &tmR, r_full + 8 * d, ahead.channel(),
+                                    static_cast<int>(ahead.row()));
                     }
                 }
+            };
+            uint32_t r_phase = 0;  // parity per box slot, one bit each
+            if (a.r)
+                ask(a.io - 1);
+            int i = 0, tile = 0;
+            bool ok = true;
+            for (; !cur.done(); ++i) {
+                const int d = i % a.io;
+                const int ch = cur.channel();
+                const long long row = cur.row();
+                const bool inside = row < a.M && ch < a.N;
+                // the box's bias, asked for ahead of the waits
+                float b0 = 0.f, b1 = 0.f;
+                if (a.bias) {
+                    b0 = ch + lane < a.N ? __ldg(a.bias + ch + lane) : 0.f;
+                    if (B::kCols == 64)
+                        b1 = ch + 32 + lane < a.N ? __ldg(a.bias + ch + 32 + lane) : 0.f;
+                }
+                if (cur.half == 0 && cur.first_of_half()) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(acc_full(tile & 1), (tile >> 1) & 1, ctl,
+                                                           kDevTimeoutEpilogue))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                // The slot is free once its last store has read it; with a shortcut
+                // the slot after this one's predecessor is refilled meanwhile.
+                if (a.r) {
+                    if (lane == 0)
+                        bulk_wait_read<1>();
+                    __syncwarp();
+                    ask(i + a.io - 1);
+                    if (inside && !__all_sync(0xffffffffu,
+                                              mbar_wait(r_full + 8 * d, (r_phase >> d) & 1, ctl,
+                                                        kDevTimeoutEpilogue))) {
+                        ok = false;
+                        break;
+                    }
+                    if (inside)
+                        r_phase ^= 1u << d;
+                } else {
+                    if (lane == 0)
+                        bulk_wait_read<1>();
+                }
+                bias[lane] = b0;
+                if (B::kCols == 64)
+                    bias[32 + lane] = b1;
                 __syncwarp();
+                const uint32_t acc = tmem + (tile & 1) * S::kSecond + cur.col() + lanes_at;
+                uint8_t *mine = boxes_p + d * kIoBox + lane * 128;
+#pragma unroll
+                for (int h = 0; h < B::kCols / 32; ++h) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32_sync(acc + 32 * h, v);
+                    // 16 bytes (kV elements) at a time
+                    constexpr int kV = 16 / sizeof(T);
+#pragma unroll
+                    for (int c = 0; c < 32; c += kV) {
+                        uint8_t *at = mine + ((((32 * h + c) / kV) ^ (lane & 7)) * 16);
+                        F2 f[kV / 2];
+#pragma unroll
+                        for (int j = 0; j < kV; j += 4) {
+                            const float4 b = *reinterpret_cast<const float4 *>(bias + 32 * h + c + j);
+                            f[j / 2] = add2(f2(__uint_as_float(v[c + j]), __uint_as_float(v[c + j + 1])),
+                                            f2(b.x, b.y));
+                            f[j / 2 + 1] = add2(f2(__uint_as_float(v[c + j + 2]),
+                                                   __uint_as_float(v[c + j + 3])),
+                                                f2(b.z, b.w));
+                        }
+                        if (a.r) {
+                            const Vec<T, kV> rv = *reinterpret_cast<const Vec<T, kV> *>(at);
+                            F2 g[kV / 2];
+                            unpack<T, kV>(rv, g);
+#pragma unroll
+                            for (int j = 0; j < kV / 2; ++j)
+                                f[j] = add2(f[j], g[j]);
+                        }
+                        store_vec<T, kV>(reinterpret_cast<T *>(at), finish<T, kV>(f, a.act));
+                    }
+                }
+                // the accumulator columns of this half (or tile) are read
+                if (S::kShared ? cur.half == 0 && cur.last_of_half() : cur.last_of_tile())
+                    release(S::kShared ? 0 : tile & 1);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (inside)
+                        tma_store_2d(&tmO, boxes + d * kIoBox, ch, static_cast<int>(row));
+                    bulk_commit();
+                }
+                if (cur.last_of_tile())
+                    ++tile;
+                cur.next();
             }
-            tc_fence_before();
+            // Shortcut boxes asked for but not used land before the CTA leaves.
+            if (a.r && !ok && lane == 0) {
+                B at = cur;
+                for (int k = i; k < n_ahead && !at.done(); ++k, at.next()) {
+                    const int d = k % a.io;
+                    if (at.row() < a.M && at.channel() < a.N) {
+                        if (!mbar_drain(r_full + 8 * d, (r_phase >> d) & 1, kDrainNs))
+                            atomicOr(a.status, kDevDrainFailed);
+                    }
+                }
+            }
+            if (side >= B::kPer) {
+                // this side has no boxes: it still answers for its share of the barrier
+                for (int t = unit, n = 0; t < a.tiles; t += units, ++n) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(acc_full(n & 1), (n >> 1) & 1, ctl,
+                                                           kDevTimeoutEpilogue)))
+                        break;
+                    release(S::kShared ? 0 : n & 1);
+                }
+            }
             if (lane == 0)
-                mbar_arrive(acc_empty(buf));
-            buf ^= 1;
-            aph ^= buf == 0;
+                bulk_wait_all();
+        } else {
+            float *patch = reinterpret_cast<float *>(smem) + e * (kPatch / 4);
+            constexpr int kHalves = S::kShared ? 2 : 1, kHalf = BN / kHalves;
+            int n = 0;
+            for (int t = unit; t < a.tiles; t += units, ++n) {
+                const int mt = t / a.n_tiles, nt = t - mt * a.n_tiles;
+                if (!__all_sync(0xffffffffu, mbar_wait(acc_full(n & 1), (n >> 1) & 1, ctl,
+                                                       kDevTimeoutEpilogue)))
+                    break;
+                tc_fence_after();
+                const long long row0 = static_cast<long long>(mt) * (kPair ? 256 : 128) + row_off;
+                const int rows = static_cast<int>(max(0ll, min(32ll, a.M - row0)));
+                for (int half = 0; half < kHalves; ++half) {
+                    const int h = S::kShared ? (half ^ (n & 1) ^ 1) : 0;
+                    const int first = h * kHalf + side * (kHalf / 2);
+                    for (int c0 = first; c0 < first + kHalf / 2; c0 += 32) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32_sync(tmem + (n & 1) * S::kSecond + c0 + lanes_at, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            patch[lane * 33 + i] = __uint_as_float(v[i]);
+                        __syncwarp();
+                        const int o = nt * BN + c0 + lane;
+                        if (o < a.N) {
+                            const float b = a.bias ? a.bias[o] : 0.f;
+                            size_t at = static_cast<size_t>(row0) * a.N + o;
+#pragma unroll 4
+                            for (int i = 0; i < rows; ++i, at += a.N) {
+                                float y = patch[i * 33 + lane] + b;
+                                if (a.r)
+                                    y += to_f(static_cast<const T *>(a.r)[at]);
+                                static_cast<T *>(a.out)[at] = from_f<T>(activate(y, a.act));
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (half == 0)
+                        release(S::kShared ? 0 : n & 1);
+                }
+            }
         }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair) {
+        // neither CTA of a pair leaves while the other may still reach it (its
+        // copies complete on rank 0's barriers, its arrivals cross over)
+        if (threadIdx.x == 0) {
+            mbar_arrive_cluster(mapa_shared(exit_bar, rank ^ 1u));
+            if (!mbar_drain(exit_bar, 0, 2 * a.wait_ns + kDrainNs))
+                atomicOr(a.status, kDevDrainFailed);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmem);
+        if (kPair)
+            tmem_dealloc_pair(tmem, kTmem);
+        else
+            tmem_dealloc(tmem, kTmem);
     }
 }
 
-template <typename T, int BN> int run(const Mx4Call &c, int sms, cudaStream_t s)
+CUtensorMapDataType map_type(int dtype)
 {
-    using S = Shape<BN>;
+    return dtype == X1CB_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+           : dtype == X1CB_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+template <typename T, int BN, bool kPair, bool kIo>
+int run(const Mx4Call &c, int sms, cudaStream_t s)
+{
+    using S = Shape<BN, kPair>;
+    constexpr int kTileM = kPair ? 256 : 128;
     MxArgs a{};
     unsigned int *forms = nullptr;
     if (int e = device_words(&a.status, &forms))
         return e;
-    a.xs = c.xs;
-    a.ws = c.ws;
     a.bias = c.bias;
     a.r = c.r;
     a.out = c.out;
@@ -279,45 +561,93 @@ template <typename T, int BN> int run(const Mx4Call &c, int sms, cudaStream_t s)
     a.inject = debug_inject();
     a.k_steps = (c.K + kStageK - 1) / kStageK;
     a.kt = (c.K + 127) / 128;
-    a.m_tiles = static_cast<int>((c.M + 127) / 128);
     a.n_tiles = (c.N + BN - 1) / BN;
-    const int fixed = 1024 + kEpiWarps * kPatch + static_cast<int>(sizeof(Tail));
-    a.stages = std::min({(232448 - fixed) / S::kStage, (kTmem - 2 * BN) / S::kSfCols, 8});
+    const long long tiles = (c.M + kTileM - 1) / kTileM * a.n_tiles;
+    if (tiles > 0x7fffffffLL)
+        return X1CB_ERR_SHAPE;
+    a.tiles = static_cast<int>(tiles);
+    // a shortcut box is asked for two boxes ahead; one where the ring needs the room
+    a.io = c.r ? (kPair || a.k_steps > 2 ? 3 : 4) : 2;
+    const int epi = (kEpiWarps * (kIo ? a.io * kIoBox : kPatch) + 1023) & ~1023;
+    const int fixed = 1024 + epi + static_cast<int>(sizeof(Tail));
+    a.stages = std::min({(232448 - fixed) / S::kStage, (kTmem - S::kSfBase) / S::kSfCols, 8});
     const int smem = fixed + a.stages * S::kStage;
-    CUtensorMap tmX, tmW;
+
+    CUtensorMap tmX, tmW, tmXs, tmWs, tmR, tmO;
     const uint64_t str[1] = {static_cast<uint64_t>(c.K) / 2};
     const uint64_t dx[2] = {str[0], static_cast<uint64_t>(c.M)};
     const uint64_t dw[2] = {str[0], static_cast<uint64_t>(c.N)};
-    const uint32_t bx[2] = {128, 128}, bw[2] = {128, BN};
+    const uint32_t bx[2] = {128, 128}, bw[2] = {128, static_cast<uint32_t>(S::kWRows)};
     if (int e = encode_map(&tmX, c.x, 2, dx, str, bx, CU_TENSOR_MAP_SWIZZLE_128B))
         return e;
     if (int e = encode_map(&tmW, c.w, 2, dw, str, bw, CU_TENSOR_MAP_SWIZZLE_128B))
         return e;
-    if (cudaFuncSetAttribute(conv_mx4_kernel<T, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             232448) != cudaSuccess)
+    // scales as rows of one tile (128 words), two tiles to a box
+    const uint64_t sstr[1] = {512};
+    const uint64_t dxs[2] = {128, static_cast<uint64_t>((c.M + 127) / 128) * a.kt};
+    const uint64_t dws[2] = {128, static_cast<uint64_t>((c.N + 127) / 128) * a.kt};
+    const uint32_t bs[2] = {128, 2};
+    if (int e = encode_map(&tmXs, c.xs, 2, dxs, sstr, bs, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_DATA_TYPE_UINT32))
+        return e;
+    if (int e = encode_map(&tmWs, c.ws, 2, dws, sstr, bs, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_DATA_TYPE_UINT32))
+        return e;
+    tmR = tmO = tmX;  // unused without kIo
+    if (kIo) {
+        const uint64_t ostr[1] = {static_cast<uint64_t>(c.N) * sizeof(T)};
+        const uint64_t d[2] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.M)};
+        const uint32_t b[2] = {128 / sizeof(T), 32};
+        if (int e = encode_map(&tmO, c.out, 2, d, ostr, b, CU_TENSOR_MAP_SWIZZLE_128B,
+                               map_type(c.dtype)))
+            return e;
+        if (c.r)
+            if (int e = encode_map(&tmR, c.r, 2, d, ostr, b, CU_TENSOR_MAP_SWIZZLE_128B,
+                                   map_type(c.dtype)))
+                return e;
+    }
+    static std::atomic<bool> opted[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return X1CB_ERR_CUDA;
-    const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
-    if (tiles > 0x7fffffffLL)
-        return X1CB_ERR_SHAPE;
+    const auto kern = conv_mx4_kernel<T, BN, kPair, kIo>;
+    if (!opted[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) !=
+            cudaSuccess)
+            return X1CB_ERR_CUDA;
+        opted[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(tiles, sms)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * std::min<long long>(tiles, sms / 2)
+                                                   : std::min<long long>(tiles, sms)),
+                       1, 1);
     cfg.blockDim = dim3(kMxThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, conv_mx4_kernel<T, BN>, tmX, tmW, a) == cudaSuccess
+    cfg.numAttrs = kPair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, tmX, tmW, tmXs, tmWs, tmR, tmO, a) == cudaSuccess
                ? X1CB_OK
                : X1CB_ERR_CUDA;
 }
 
-template <typename T> int run_bn(const Mx4Call &c, int sms, cudaStream_t s)
+template <typename T> int run_tile(const Mx4Call &c, int sms, cudaStream_t s)
 {
-    return c.N <= 64 ? run<T, 64>(c, sms, s) : run<T, 128>(c, sms, s);
+    const bool io = static_cast<size_t>(c.N) * sizeof(T) % 16 == 0;
+    if (c.N <= 64)
+        return io ? run<T, 64, false, true>(c, sms, s) : run<T, 64, false, false>(c, sms, s);
+    const long long pairs = (c.M + 255) / 256 * ((c.N + 255) / 256);
+    if (pairs >= sms / 2)
+        return io ? run<T, 256, true, true>(c, sms, s) : run<T, 256, true, false>(c, sms, s);
+    return io ? run<T, 128, false, true>(c, sms, s) : run<T, 128, false, false>(c, sms, s);
 }
 
 }  // namespace
@@ -327,9 +657,9 @@ int launch_conv_mx4_tiles(const Mx4Call &c, cudaStream_t s)
     int sms = 0;
     if (int e = current_sms(sms))
         return e;
-    return c.dtype == X1CB_F32    ? run_bn<float>(c, sms, s)
-           : c.dtype == X1CB_BF16 ? run_bn<__nv_bfloat16>(c, sms, s)
-                                  : run_bn<__half>(c, sms, s);
+    return c.dtype == X1CB_F32    ? run_tile<float>(c, sms, s)
+           : c.dtype == X1CB_BF16 ? run_tile<__nv_bfloat16>(c, sms, s)
+                                  : run_tile<__half>(c, sms, s);
 }
 
 }  // namespace x1cb
