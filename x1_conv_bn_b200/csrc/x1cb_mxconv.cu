@@ -8,13 +8,18 @@
 //               swizzle) and their scale tiles (512 bytes per 128 rows x 128 K,
 //               stored in the order TMEM wants them) into a ring of stages;
 //   warp 1      (of rank 0) copies the scales to TMEM (tcgen05.cp) and issues the
-//               MMAs, four K = 64 steps a stage.  The scale columns belong to the
-//               stage, so they are free exactly when the stage is;
-//   warps 4-11  epilogue: two warps per TMEM lane quarter, from two accumulators
-//               in turn, so that it runs beside the next tile's MMAs.  The pair's
-//               two accumulators of 256 columns share 128 columns (TMEM has 512,
-//               and the scales need theirs): the shared half is drained first and
-//               the next tile starts when it is free.
+//               MMAs, four K = 64 steps a stage;
+//   warps 4-..  epilogue: groups of eight warps, two per TMEM lane quarter, on two
+//               accumulators in turn, so that it runs beside the next tile's MMAs.
+// One CTA: two groups, an accumulator each.  A warp's way through a box (TMEM,
+// shared memory, store) is one long chain of latencies, and two groups keep two
+// tiles in it (200704 x 128 x 512: 61.6 us with one group, 50.9 with two).
+// Pair: one group (its K loop is long enough to hide the epilogue behind).  TMEM
+// has 512 columns, and the scales need theirs: the accumulators of 256 share
+// 128, which are drained first, and the next tile's MMAs start when they are in
+// registers.  The scale columns belong to the ring stage and are free exactly
+// when it is (two buffers for all stages, so that only 64 columns were shared,
+// made the MMAs wait for one another: 16384 x 4096 x 4096 183 us, not KKK).
 // Every wait is bounded: on a timeout the CTA raises an abort flag, records a
 // status bit, lets its copies and MMAs land and leaves.
 #include <cuda_runtime.h>
@@ -32,14 +37,14 @@
 namespace x1cb {
 namespace {
 
-constexpr int kEpiWarps = 8;
-constexpr int kMxThreads = 32 * (4 + kEpiWarps);
+constexpr int kGroupWarps = 8;
+constexpr int kMaxEpiWarps = 16;
 constexpr int kStageK = 256;           // elements: 128 bytes of codes a row
 constexpr int kRowsBytes = 128 * 128;  // codes of 128 rows in a stage
 constexpr int kSfBytes = 1024;         // scales of 128 rows in a stage
 constexpr int kTmem = 512;
 constexpr int kIoBox = 32 * 128;       // an epilogue warp's 32 rows x 128 bytes
-constexpr int kMaxIo = 4;              // such boxes per warp
+constexpr int kMaxIo = 2;              // such boxes per warp
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct MxArgs {
@@ -61,53 +66,54 @@ template <int BN, bool kPair> struct Shape {
     static constexpr int kW = kWRows * 128;           // weight codes of a stage
     static constexpr int kStage = kRowsBytes + kW + kSfBytes * (1 + kBlocks);
     static constexpr int kSfCols = 8 + kBlocks * 8;   // TMEM columns a stage's scales take
-    static constexpr bool kShared = BN == 256;        // accumulators that share columns
-    static constexpr int kSecond = kShared ? 128 : BN;  // first column of accumulator 1
+    static constexpr int kSharedCols = kPair ? 128 : 0;
+    static constexpr int kSecond = BN - kSharedCols;  // first column of accumulator 1
     static constexpr int kSfBase = kSecond + BN;
+    static constexpr int kSfStages = (kTmem - kSfBase) / kSfCols;  // most ring stages
+    static constexpr int kGroups = kPair ? 1 : 2;     // epilogue groups
+    static constexpr int kEpiWarps = kGroups * kGroupWarps;
+    static constexpr int kThreads = 32 * (4 + kEpiWarps);
 };
 
 // Tail of the dynamic shared memory behind the ring and the epilogue's boxes.
 constexpr int kPatch = 32 * 33 * 4;  // an epilogue warp's transposing patch (plain epilogue)
 struct Tail {
-    alignas(16) float bias[kEpiWarps][64];  // read four at a time
-    unsigned long long bars[2 * 8 + 2 * 2 + 3];
-    unsigned long long r_full[kEpiWarps][kMaxIo];
+    alignas(16) float bias[kMaxEpiWarps][64];  // read four at a time
+    unsigned long long bars[2 * 8 + 2 * 2 + 4];
+    unsigned long long r_full[kMaxEpiWarps][kMaxIo];
     uint32_t tmem;
     int abort_flag;
 };
 
 // The boxes of 32 rows x 128 bytes that an epilogue warp works through, in
-// order: the tiles of the CTA, per tile the halves of 128 channels (shared
-// accumulator columns first), per half the boxes of the warp's side.
+// order: the tiles of its group, per tile every second box (the warp's side),
+// from the columns that the accumulators share on.
 template <typename T, int BN, bool kPair> struct Boxes {
     using S = Shape<BN, kPair>;
     static constexpr int kCols = 128 / sizeof(T);
-    static constexpr int kHalves = S::kShared ? 2 : 1;
-    static constexpr int kHalf = BN / kHalves;
-    static constexpr int kPer = kHalf / kCols;  // boxes per half, both sides
-    int t, step, end, n_tiles, side, row_off;
-    int half, box, parity;
+    static constexpr int kPer = BN / kCols;                  // boxes per tile, both sides
+    int t, step, end, n_tiles, acc, side, row_off;
+    int j;
 
-    __device__ __forceinline__ Boxes(const MxArgs &a, int unit, int units, int side_, int row_off_)
-        : t(unit), step(units), end(a.tiles), n_tiles(a.n_tiles), side(side_), row_off(row_off_),
-          half(0), box(side_), parity(0)
+    __device__ __forceinline__ Boxes(const MxArgs &a, int unit, int units, int group, int side_,
+                                     int row_off_)
+        : t(unit + group * units), step(S::kGroups * units), end(a.tiles), n_tiles(a.n_tiles),
+          acc(group), side(side_), row_off(row_off_), j(side_)
     {
-        if (box >= kPer)
+        if (j >= kPer)
             t = end;  // a side without boxes
     }
     __device__ __forceinline__ bool done() const { return t >= end; }
-    __device__ __forceinline__ bool first_of_half() const { return box == side; }
-    __device__ __forceinline__ bool last_of_half() const { return box + 2 >= kPer; }
-    __device__ __forceinline__ bool last_of_tile() const
+    __device__ __forceinline__ bool first_of_tile() const { return j == side; }
+    __device__ __forceinline__ bool last_of_tile() const { return j + 2 >= kPer; }
+    // the warp's last box in the shared columns
+    __device__ __forceinline__ bool last_shared() const
     {
-        return half == kHalves - 1 && last_of_half();
+        return j < S::kSharedCols / kCols && j + 2 >= S::kSharedCols / kCols;
     }
-    // first column within the tile
-    __device__ __forceinline__ int col() const
-    {
-        const int h = S::kShared ? (half ^ parity ^ 1) : 0;  // accumulator 0: upper half first
-        return h * kHalf + box * kCols;
-    }
+    // first column within the tile: accumulator 0 shares its last columns with
+    // the first of accumulator 1
+    __device__ __forceinline__ int col() const { return (acc ? j : kPer - 1 - j) * kCols; }
     __device__ __forceinline__ int channel() const { return t % n_tiles * BN + col(); }
     __device__ __forceinline__ long long row() const
     {
@@ -115,15 +121,13 @@ template <typename T, int BN, bool kPair> struct Boxes {
     }
     __device__ __forceinline__ void next()
     {
-        box += 2;
-        if (box < kPer)
+        j += 2;
+        if (j < kPer)
             return;
-        box = side;
-        if (++half == kHalves) {
-            half = 0;
-            t += step;
-            parity ^= 1;
-        }
+        j = side;
+        t += step;
+        if (S::kGroups == 1)
+            acc ^= 1;
     }
 };
 
@@ -131,7 +135,7 @@ template <typename T, int BN, bool kPair> struct Boxes {
 // needs rows of a multiple of 16 bytes; otherwise the plain epilogue transposes
 // through shared memory and stores element by element.
 template <typename T, int BN, bool kPair, bool kIo>
-__global__ void __launch_bounds__(kMxThreads, 1)
+__global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
     conv_mx4_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmXs,
                     const __grid_constant__ CUtensorMap tmWs,
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                                                 ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     // the epilogue's boxes first: they keep the 1024-byte alignment of the swizzle
-    const int epi_bytes = kEpiWarps * (kIo ? a.io * kIoBox : kPatch);
+    const int epi_bytes = S::kEpiWarps * (kIo ? a.io * kIoBox : kPatch);
     const uint32_t ring = sbase + ((epi_bytes + 1023) & ~1023);
     Tail *tail = reinterpret_cast<Tail *>(smem + (ring - sbase) + a.stages * S::kStage);
     const uint32_t bars = smem_u32(tail->bars);
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const auto acc_full = [&](int b) { return bars + 8u * (2 * a.stages + b); };
     const auto acc_empty = [&](int b) { return bars + 8u * (2 * a.stages + 2 + b); };
     const uint32_t mma_done = bars + 8u * (2 * a.stages + 4), never = mma_done + 8u;
-    const uint32_t exit_bar = never + 8u;
+    const uint32_t exit_bar = never + 8u, shared_free = never + 16u;
     volatile int *abort_flag = &tail->abort_flag;
     const WaitCtl ctl{abort_flag, a.status, a.inject == 1 ? 4 * a.wait_ns : a.wait_ns};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -169,9 +173,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), kEpiWarps * (kPair ? 2 : 1));
+            mbar_init(acc_empty(b), kGroupWarps * (kPair ? 2 : 1));
         }
-        for (int w = 0; w < kEpiWarps; ++w)
+        mbar_init(shared_free, 2 * kGroupWarps);  // of both CTAs
+        for (int w = 0; w < S::kEpiWarps; ++w)
             for (int b = 0; b < kMaxIo; ++b)
                 mbar_init(smem_u32(&tail->r_full[w][b]), 1);
         mbar_init(mma_done, 1);
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     if (kPair)  // both CTAs' barriers and TMEM exist before traffic crosses
         cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem = tail->tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tail->tmem, 0);
     griddep_wait();  // from here on global memory is touched
 
     if (warp == 0) {
@@ -275,10 +280,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         int s = 0, i = 0;
         uint32_t ph = 0;
         for (int t = unit; ok && t < a.tiles; t += units, ++i) {
-            // The accumulator is free: its own last tile is drained, or with shared
-            // columns the tile before this one has left them.
-            if (S::kShared ? i > 0 && !wait(acc_empty(0), (i - 1) & 1)
-                           : !wait(acc_empty(i & 1), ((i >> 1) & 1) ^ 1))
+            // The accumulator is free: its own last tile is drained, and the tile
+            // before this one has left the shared columns.
+            if (!wait(acc_empty(i & 1), ((i >> 1) & 1) ^ 1) ||
+                (kPair && i > 0 && !wait(shared_free, (i - 1) & 1)))
                 break;
             tc_fence_after();
             const uint32_t d = tmem + (i & 1) * S::kSecond;
@@ -292,20 +297,27 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 tc_fence_after();
                 const uint32_t st = ring + s * S::kStage, sf = st + kRowsBytes + S::kW;
                 const uint32_t sfa = tmem + S::kSfBase + s * S::kSfCols, sfw = sfa + 8;
-                const int left = min(4, (a.K - k * kStageK + 63) / 64);
-                for (int j = 0; j < (left + 1) / 2; ++j) {
-                    tmem_cp_scales<kPair>(sfa + 4 * j, smem_desc_scales(sf + 512 * j));
-#pragma unroll
-                    for (int b = 0; b < S::kBlocks; ++b)
-                        tmem_cp_scales<kPair>(sfw + S::kBlocks * 4 * j + 4 * b,
-                                              smem_desc_scales(sf + kSfBytes * (1 + b) + 512 * j));
-                }
                 const uint64_t ad = smem_desc_sw128(st), bd = smem_desc_sw128(st + kRowsBytes);
-                for (int j = 0; j < left; ++j)
-                    mma_mx4<kPair>(d, ad + 2 * j, bd + 2 * j,
-                                   idesc_mx4(kPair ? 256 : 128, BN, (j & 1) * 2),
-                                   sfa + 4 * (j >> 1), sfw + S::kBlocks * 4 * (j >> 1) + half,
-                                   k > 0 || j > 0);
+                constexpr uint32_t kM = kPair ? 256 : 128;
+                const int left = (a.K - k * kStageK + 63) / 64;  // K = 64 steps
+                if (left >= 4) {
+                    mma_mx4_stage<kPair, S::kBlocks>(d, ad, bd, idesc_mx4(kM, BN, 0),
+                                                     idesc_mx4(kM, BN, 2), sfa, sfw, half,
+                                                     smem_desc_scales(sf), k > 0);
+                } else {
+                    for (int j = 0; j < (left + 1) / 2; ++j) {
+                        tmem_cp_scales<kPair>(sfa + 4 * j, smem_desc_scales(sf + 512 * j));
+#pragma unroll
+                        for (int b = 0; b < S::kBlocks; ++b)
+                            tmem_cp_scales<kPair>(
+                                sfw + S::kBlocks * 4 * j + 4 * b,
+                                smem_desc_scales(sf + kSfBytes * (1 + b) + 512 * j));
+                    }
+                    for (int j = 0; j < left; ++j)
+                        mma_mx4<kPair>(d, ad + 2 * j, bd + 2 * j, idesc_mx4(kM, BN, (j & 1) * 2),
+                                       sfa + 4 * (j >> 1), sfw + S::kBlocks * 4 * (j >> 1) + half,
+                                       k > 0 || j > 0);
+                }
                 commit(empty(s));
                 if (++s == a.stages) {
                     s = 0;
@@ -322,18 +334,26 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             atomicOr(a.status, kDevDrainFailed);
         __syncwarp();
     } else if (warp >= 4) {
-        const int e = warp - 4, quarter = e & 3, side = e >> 2;
-        const uint32_t lanes_at = static_cast<uint32_t>(quarter * 32) << 16;
+        const int e = warp - 4, quarter = e & 3, side = (e >> 2) & 1, group = e >> 3;
+        const uint32_t lanes_at = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const int row_off = static_cast<int>(rank) * 128 + quarter * 32;
-        const auto release = [&](int b) {  // after the warp's reads of an accumulator
+        const auto release = [&](uint32_t bar) {  // after the warp's reads of the accumulator
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if (kPair)
-                    mbar_arrive_cluster(mapa_shared(acc_empty(b), 0));
+                    mbar_arrive_cluster(mapa_shared(bar, 0));
                 else
-                    mbar_arrive(acc_empty(b));
+                    mbar_arrive(bar);
             }
+        };
+        uint32_t acc_phase = 0;  // parity per accumulator, one bit each
+        const auto wait_acc = [&](int acc) {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full(acc), (acc_phase >> acc) & 1,
+                                                              ctl, kDevTimeoutEpilogue));
+            acc_phase ^= 1u << acc;
+            tc_fence_after();
+            return ok;
         };
         if constexpr (kIo) {
             using B = Boxes<T, BN, kPair>;
@@ -341,13 +361,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             uint8_t *boxes_p = smem + e * a.io * kIoBox;
             float *bias = tail->bias[e];
             const uint32_t r_full = smem_u32(tail->r_full[e]);
-            B cur(a, unit, units, side, row_off), ahead = cur;
+            B cur(a, unit, units, group, side, row_off), ahead = cur;
             int n_ahead = 0;  // shortcut boxes asked for so far
             const auto ask = [&](int most) {
                 // ask for shortcut boxes up to (not including) number `most`
                 for (; n_ahead < most && !ahead.done(); ++n_ahead, ahead.next()) {
                     if (lane == 0 && ahead.row() < a.M && ahead.channel() < a.N) {
-                        const int d = n_ahead % a.io;
+                        const int d = a.io == 2 ? n_ahead & 1 : 0;
                         mbar_arrive_expect_tx(r_full + 8 * d, kIoBox);
                         tma_load_2d(boxes + d * kIoBox, &tmR, r_full + 8 * d, ahead.channel(),
                                     static_cast<int>(ahead.row()));
@@ -355,59 +375,80 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 }
             };
             uint32_t r_phase = 0;  // parity per box slot, one bit each
-            if (a.r)
-                ask(a.io - 1);
-            int i = 0, tile = 0;
-            bool ok = true;
-            for (; !cur.done(); ++i) {
-                const int d = i % a.io;
-                const int ch = cur.channel();
-                const long long row = cur.row();
-                const bool inside = row < a.M && ch < a.N;
-                // the box's bias, asked for ahead of the waits
-                float b0 = 0.f, b1 = 0.f;
-                if (a.bias) {
-                    b0 = ch + lane < a.N ? __ldg(a.bias + ch + lane) : 0.f;
+            // a box's bias is loaded one box ahead, two channels a lane
+            float b0 = 0.f, b1 = 0.f;
+            const auto load_bias = [&](const B &at) {
+                if (a.bias && !at.done()) {
+                    const int c = at.channel() + lane;
+                    b0 = c < a.N ? __ldg(a.bias + c) : 0.f;
                     if (B::kCols == 64)
-                        b1 = ch + 32 + lane < a.N ? __ldg(a.bias + ch + 32 + lane) : 0.f;
+                        b1 = c + 32 < a.N ? __ldg(a.bias + c + 32) : 0.f;
                 }
-                if (cur.half == 0 && cur.first_of_half()) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(acc_full(tile & 1), (tile >> 1) & 1, ctl,
+            };
+            load_bias(cur);
+            int i = 0;
+            bool ok = true;
+            B now = cur;
+            for (; !cur.done(); ++i) {
+                now = cur;
+                cur.next();
+                const int d = a.io == 2 ? i & 1 : 0;
+                const int ch = now.channel();
+                const long long row = now.row();
+                const bool inside = row < a.M && ch < a.N;
+                // A slot is free once its last store has read it.
+                if (lane == 0) {
+                    if (a.r || a.io == 1)
+                        bulk_wait_read<0>();
+                    else
+                        bulk_wait_read<1>();
+                }
+                if (a.r) {
+                    __syncwarp();
+                    ask(i + a.io);
+                }
+                if (now.first_of_tile() && !wait_acc(now.acc)) {
+                    ok = false;
+                    break;
+                }
+                if (a.r && inside) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(r_full + 8 * d, (r_phase >> d) & 1, ctl,
                                                            kDevTimeoutEpilogue))) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
+                    r_phase ^= 1u << d;
                 }
-                // The slot is free once its last store has read it; with a shortcut
-                // the slot after this one's predecessor is refilled meanwhile.
-                if (a.r) {
-                    if (lane == 0)
-                        bulk_wait_read<1>();
-                    __syncwarp();
-                    ask(i + a.io - 1);
-                    if (inside && !__all_sync(0xffffffffu,
-                                              mbar_wait(r_full + 8 * d, (r_phase >> d) & 1, ctl,
-                                                        kDevTimeoutEpilogue))) {
-                        ok = false;
-                        break;
-                    }
-                    if (inside)
-                        r_phase ^= 1u << d;
-                } else {
-                    if (lane == 0)
-                        bulk_wait_read<1>();
+                // Pair: the box's columns are read at once, and the accumulator (or
+                // its shared part) handed back before the arithmetic.  One CTA with
+                // two groups has the registers for 32 columns at a time.
+                const uint32_t acc = lanes_at + now.acc * S::kSecond + now.col();
+                uint32_t v[kPair ? B::kCols / 32 : 1][32];
+                if constexpr (kPair) {
+#pragma unroll
+                    for (int h = 0; h < B::kCols / 32; ++h)
+                        tmem_ld_32x32b_x32(acc + 32 * h, v[h]);
                 }
                 bias[lane] = b0;
                 if (B::kCols == 64)
                     bias[32 + lane] = b1;
+                load_bias(cur);
+                if constexpr (kPair) {
+#pragma unroll
+                    for (int h = 0; h < B::kCols / 32; ++h)
+                        tmem_ld_wait(v[h]);
+                    if (now.last_shared())
+                        release(shared_free);
+                    if (now.last_of_tile())
+                        release(acc_empty(now.acc));
+                }
                 __syncwarp();
-                const uint32_t acc = tmem + (tile & 1) * S::kSecond + cur.col() + lanes_at;
                 uint8_t *mine = boxes_p + d * kIoBox + lane * 128;
 #pragma unroll
                 for (int h = 0; h < B::kCols / 32; ++h) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32_sync(acc + 32 * h, v);
+                    if constexpr (!kPair)
+                        tmem_ld_32x32b_x32_sync(acc + 32 * h, v[0]);
+                    const uint32_t(&w)[32] = v[kPair ? h : 0];
                     // 16 bytes (kV elements) at a time
                     constexpr int kV = 16 / sizeof(T);
 #pragma unroll
@@ -417,10 +458,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 #pragma unroll
                         for (int j = 0; j < kV; j += 4) {
                             const float4 b = *reinterpret_cast<const float4 *>(bias + 32 * h + c + j);
-                            f[j / 2] = add2(f2(__uint_as_float(v[c + j]), __uint_as_float(v[c + j + 1])),
+                            f[j / 2] = add2(f2(__uint_as_float(w[c + j]), __uint_as_float(w[c + j + 1])),
                                             f2(b.x, b.y));
-                            f[j / 2 + 1] = add2(f2(__uint_as_float(v[c + j + 2]),
-                                                   __uint_as_float(v[c + j + 3])),
+                            f[j / 2 + 1] = add2(f2(__uint_as_float(w[c + j + 2]),
+                                                   __uint_as_float(w[c + j + 3])),
                                                 f2(b.z, b.w));
                         }
                         if (a.r) {
@@ -434,9 +475,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         store_vec<T, kV>(reinterpret_cast<T *>(at), finish<T, kV>(f, a.act));
                     }
                 }
-                // the accumulator columns of this half (or tile) are read
-                if (S::kShared ? cur.half == 0 && cur.last_of_half() : cur.last_of_tile())
-                    release(S::kShared ? 0 : tile & 1);
+                if (!kPair && now.last_of_tile())
+                    release(acc_empty(now.acc));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -444,16 +484,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         tma_store_2d(&tmO, boxes + d * kIoBox, ch, static_cast<int>(row));
                     bulk_commit();
                 }
-                if (cur.last_of_tile())
-                    ++tile;
-                cur.next();
             }
             // Shortcut boxes asked for but not used land before the CTA leaves.
             if (a.r && !ok && lane == 0) {
-                B at = cur;
-                for (int k = i; k < n_ahead && !at.done(); ++k, at.next()) {
-                    const int d = k % a.io;
-                    if (at.row() < a.M && at.channel() < a.N) {
+                for (int k = i; k < n_ahead && !now.done(); ++k, now.next()) {
+                    const int d = a.io == 2 ? k & 1 : 0;
+                    if (now.row() < a.M && now.channel() < a.N) {
                         if (!mbar_drain(r_full + 8 * d, (r_phase >> d) & 1, kDrainNs))
                             atomicOr(a.status, kDevDrainFailed);
                     }
@@ -461,54 +497,49 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
             if (side >= B::kPer) {
                 // this side has no boxes: it still answers for its share of the barrier
-                for (int t = unit, n = 0; t < a.tiles; t += units, ++n) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(acc_full(n & 1), (n >> 1) & 1, ctl,
-                                                           kDevTimeoutEpilogue)))
-                        break;
-                    release(S::kShared ? 0 : n & 1);
-                }
+                // (only a 64-channel tile of one CTA: no shared columns)
+                for (int t = unit + group * units; t < a.tiles && wait_acc(group); t += 2 * units)
+                    release(acc_empty(group));
             }
             if (lane == 0)
                 bulk_wait_all();
         } else {
             float *patch = reinterpret_cast<float *>(smem) + e * (kPatch / 4);
-            constexpr int kHalves = S::kShared ? 2 : 1, kHalf = BN / kHalves;
-            int n = 0;
-            for (int t = unit; t < a.tiles; t += units, ++n) {
+            constexpr int kParts = BN / 64;  // of 64 columns, 32 for each side
+            int acc = group;
+            for (int t = unit + group * units; t < a.tiles && wait_acc(acc);
+                 t += S::kGroups * units) {
                 const int mt = t / a.n_tiles, nt = t - mt * a.n_tiles;
-                if (!__all_sync(0xffffffffu, mbar_wait(acc_full(n & 1), (n >> 1) & 1, ctl,
-                                                       kDevTimeoutEpilogue)))
-                    break;
-                tc_fence_after();
                 const long long row0 = static_cast<long long>(mt) * (kPair ? 256 : 128) + row_off;
                 const int rows = static_cast<int>(max(0ll, min(32ll, a.M - row0)));
-                for (int half = 0; half < kHalves; ++half) {
-                    const int h = S::kShared ? (half ^ (n & 1) ^ 1) : 0;
-                    const int first = h * kHalf + side * (kHalf / 2);
-                    for (int c0 = first; c0 < first + kHalf / 2; c0 += 32) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32_sync(tmem + (n & 1) * S::kSecond + c0 + lanes_at, v);
+                for (int part = 0; part < kParts; ++part) {
+                    // the shared columns first
+                    const int c0 = (acc ? part : kParts - 1 - part) * 64 + side * 32;
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32_sync(lanes_at + acc * S::kSecond + c0, v);
+                    if (part == S::kSharedCols / 64 - 1)
+                        release(shared_free);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            patch[lane * 33 + i] = __uint_as_float(v[i]);
-                        __syncwarp();
-                        const int o = nt * BN + c0 + lane;
-                        if (o < a.N) {
-                            const float b = a.bias ? a.bias[o] : 0.f;
-                            size_t at = static_cast<size_t>(row0) * a.N + o;
+                    for (int i = 0; i < 32; ++i)
+                        patch[lane * 33 + i] = __uint_as_float(v[i]);
+                    __syncwarp();
+                    const int o = nt * BN + c0 + lane;
+                    if (o < a.N) {
+                        const float b = a.bias ? a.bias[o] : 0.f;
+                        size_t at = static_cast<size_t>(row0) * a.N + o;
 #pragma unroll 4
-                            for (int i = 0; i < rows; ++i, at += a.N) {
-                                float y = patch[i * 33 + lane] + b;
-                                if (a.r)
-                                    y += to_f(static_cast<const T *>(a.r)[at]);
-                                static_cast<T *>(a.out)[at] = from_f<T>(activate(y, a.act));
-                            }
+                        for (int i = 0; i < rows; ++i, at += a.N) {
+                            float y = patch[i * 33 + lane] + b;
+                            if (a.r)
+                                y += to_f(static_cast<const T *>(a.r)[at]);
+                            static_cast<T *>(a.out)[at] = from_f<T>(activate(y, a.act));
                         }
-                        __syncwarp();
                     }
-                    if (half == 0)
-                        release(S::kShared ? 0 : n & 1);
+                    __syncwarp();
                 }
+                release(acc_empty(acc));
+                if (S::kGroups == 1)
+                    acc ^= 1;
             }
         }
         __syncwarp();
@@ -566,11 +597,14 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
     if (tiles > 0x7fffffffLL)
         return X1CB_ERR_SHAPE;
     a.tiles = static_cast<int>(tiles);
-    // a shortcut box is asked for two boxes ahead; one where the ring needs the room
-    a.io = c.r ? (kPair || a.k_steps > 2 ? 3 : 4) : 2;
-    const int epi = (kEpiWarps * (kIo ? a.io * kIoBox : kPatch) + 1023) & ~1023;
+    // With a shortcut and a short K two boxes per epilogue warp: the next shortcut
+    // box arrives beside the current one (200704 x 128 x 512: 79.9 us, with one box
+    // 84.1).  Otherwise one: a deeper ring is worth more (200704 x 512 x 128 without
+    // a shortcut 23.3 us, with two boxes 29.6).
+    a.io = !kPair && c.r && a.k_steps <= 2 ? 2 : 1;
+    const int epi = (S::kEpiWarps * (kIo ? a.io * kIoBox : kPatch) + 1023) & ~1023;
     const int fixed = 1024 + epi + static_cast<int>(sizeof(Tail));
-    a.stages = std::min({(232448 - fixed) / S::kStage, (kTmem - S::kSfBase) / S::kSfCols, 8});
+    a.stages = std::min({(232448 - fixed) / S::kStage, S::kSfStages, 8});
     const int smem = fixed + a.stages * S::kStage;
 
     CUtensorMap tmX, tmW, tmXs, tmWs, tmR, tmO;
@@ -622,7 +656,7 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
     cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * std::min<long long>(tiles, sms / 2)
                                                    : std::min<long long>(tiles, sms)),
                        1, 1);
-    cfg.blockDim = dim3(kMxThreads, 1, 1);
+    cfg.blockDim = dim3(S::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -645,7 +679,7 @@ template <typename T> int run_tile(const Mx4Call &c, int sms, cudaStream_t s)
     if (c.N <= 64)
         return io ? run<T, 64, false, true>(c, sms, s) : run<T, 64, false, false>(c, sms, s);
     const long long pairs = (c.M + 255) / 256 * ((c.N + 255) / 256);
-    if (pairs >= sms / 2)
+    if (pairs >= sms / 2 && c.K >= 1024)
         return io ? run<T, 256, true, true>(c, sms, s) : run<T, 256, true, false>(c, sms, s);
     return io ? run<T, 128, false, true>(c, sms, s) : run<T, 128, false, false>(c, sms, s);
 }

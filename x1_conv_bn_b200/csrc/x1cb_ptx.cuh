@@ -520,6 +520,39 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32_sync(uint32_t taddr, uint32_t
         : "memory");
 }
 
+// tcgen05.ld as above without its wait, for several loads in flight; the
+// registers are defined after tmem_ld_wait on the same array.
+__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+        "[%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.wait::ld.sync.aligned;"
+        : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+          "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+          "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
+          "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+          "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]),
+          "+r"(v[31])
+        :
+        : "memory");
+}
+
 // ---- pairs of CTAs (a cluster of two sharing one tcgen05 MMA) --------------
 //
 // With cta_group::2 one MMA spans the two CTAs of a cluster: A is split by rows
@@ -795,6 +828,56 @@ __device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_
             "[%5], [%6], p;\n\t}" ::"r"(d_tmem),
             "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
             : "memory");
+}
+
+// A whole ring stage of K = 256 in one go: the scale copies of both K = 128
+// halves (one tile of A, BLOCKS tiles of B each) and the four MMA steps, issued
+// by one elected lane.  sfa / sfb: the stage's scale columns; sd: descriptor of
+// its first scale tile (A's two tiles, then two per block of B; 512 bytes each);
+// sb_off: added to the scale columns of B in the MMAs.  As single wrappers, with
+// an election and operand set-up each, the ten instructions took twice the time
+// of the MMAs themselves.
+template <bool kPair, int BLOCKS>
+__device__ __forceinline__ void mma_mx4_stage(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc0, uint32_t idesc2, uint32_t sfa,
+                                              uint32_t sfb, uint32_t sb_off, uint64_t sd,
+                                              uint32_t accumulate)
+{
+#define X1CB_MX4_STAGE(CG, CPB)                                                                   \
+    asm volatile(                                                                                 \
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 s, a, b;\n\t.reg .b32 t, u, v;\n\t"                  \
+        "elect.sync _|e, 0xffffffff;\n\t"                                                         \
+        "setp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"                                      \
+        "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [%5], %8;\n\t"                            \
+        "add.s64 s, %8, 32;\n\tadd.u32 t, %5, 4;\n\t"                                            \
+        "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [t], s;\n\t" CPB                           \
+        "add.u32 u, %6, %7;\n\t"                                                                  \
+        "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "  \
+        "[%5], [u], p;\n\t"                                                                       \
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"                                             \
+        "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, "    \
+        "[%5], [u], q;\n\t"                                                                       \
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\tadd.u32 v, u, %10;\n\t"                      \
+        "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, "    \
+        "[t], [v], q;\n\t"                                                                        \
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"                                             \
+        "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, "    \
+        "[t], [v], q;\n\t}" ::"r"(d_tmem),                                                        \
+        "l"(adesc), "l"(bdesc), "r"(idesc0), "r"(idesc2), "r"(sfa), "r"(sfb), "r"(sb_off),        \
+        "l"(sd), "r"(accumulate), "n"(BLOCKS * 4)                                                 \
+        : "memory")
+#define X1CB_CP(CG, COL, TILE)                                                                    \
+    "add.s64 s, %8, " TILE ";\n\tadd.u32 u, %6, " COL ";\n\t"                                     \
+    "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [u], s;\n\t"
+    if constexpr (kPair) {
+        static_assert(!kPair || BLOCKS == 2, "");
+        X1CB_MX4_STAGE("2", X1CB_CP("2", "0", "64") X1CB_CP("2", "4", "128")
+                                X1CB_CP("2", "8", "96") X1CB_CP("2", "12", "160"));
+    } else {
+        X1CB_MX4_STAGE("1", X1CB_CP("1", "0", "64") X1CB_CP("1", "4", "96"));
+    }
+#undef X1CB_CP
+#undef X1CB_MX4_STAGE
 }
 
 }  // namespace x1cb
