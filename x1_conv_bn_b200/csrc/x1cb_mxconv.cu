@@ -8,18 +8,27 @@
 //               swizzle) and their scale tiles (512 bytes per 128 rows x 128 K,
 //               stored in the order TMEM wants them) into a ring of stages;
 //   warp 1      (of rank 0) copies the scales to TMEM (tcgen05.cp) and issues the
-//               MMAs, four K = 64 steps a stage;
-//   warps 4-..  epilogue: groups of eight warps, two per TMEM lane quarter, on two
-//               accumulators in turn, so that it runs beside the next tile's MMAs.
-// One CTA: two groups, an accumulator each.  A warp's way through a box (TMEM,
-// shared memory, store) is one long chain of latencies, and two groups keep two
-// tiles in it (200704 x 128 x 512: 61.6 us with one group, 50.9 with two).
+//               MMAs, four K = 64 steps a stage.  The scale columns belong to the
+//               ring stage and are free exactly when it is.  Of rank 1: passes its
+//               epilogue's hand-backs on to rank 0 (an arrival that releases at
+//               cluster scope costs 700 cycles in the epilogue's way);
+//   warps 4-..  epilogue: groups of eight warps, two per TMEM lane quarter, the
+//               groups and the accumulators taking the tiles in turn, so that it
+//               runs beside the next tiles' MMAs.  Results (and shortcut values
+//               before them) pass through boxes of 128 rows x 128 bytes, a stream
+//               of boxes for each group and side;
+//   warp 2      loads the shortcut into free boxes (TMA); warp 3 and the last warp
+//               store the finished ones of a side each: issuing a tensor copy
+//               costs a thread several hundred cycles, which the epilogue warps
+//               do not have.
+// One CTA: two groups and three accumulators.  A warp's way through a box (TMEM,
+// arithmetic, shared memory) is one long chain of latencies, and so is the way
+// from a drained accumulator to the next one that is full; two groups keep two
+// tiles in the first, the third accumulator hides the second.
 // Pair: one group (its K loop is long enough to hide the epilogue behind).  TMEM
-// has 512 columns, and the scales need theirs: the accumulators of 256 share
+// has 512 columns, and the scales need theirs: two accumulators of 256 share
 // 128, which are drained first, and the next tile's MMAs start when they are in
-// registers.  The scale columns belong to the ring stage and are free exactly
-// when it is (two buffers for all stages, so that only 64 columns were shared,
-// made the MMAs wait for one another: 16384 x 4096 x 4096 183 us, not KKK).
+// registers.
 // Every wait is bounded: on a timeout the CTA raises an abort flag, records a
 // status bit, lets its copies and MMAs land and leaves.
 #include <cuda_runtime.h>
@@ -43,8 +52,8 @@ constexpr int kStageK = 256;           // elements: 128 bytes of codes a row
 constexpr int kRowsBytes = 128 * 128;  // codes of 128 rows in a stage
 constexpr int kSfBytes = 1024;         // scales of 128 rows in a stage
 constexpr int kTmem = 512;
-constexpr int kIoBox = 32 * 128;       // an epilogue warp's 32 rows x 128 bytes
-constexpr int kMaxIo = 2;              // such boxes per warp
+constexpr int kIoBox = 128 * 128;      // a box: 128 rows x 128 bytes
+constexpr int kMaxIo = 2;              // boxes per stream
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct MxArgs {
@@ -57,7 +66,7 @@ struct MxArgs {
     int K, N, act, inject;
     int stages, k_steps, kt;  // ring depth; K steps of 256; scale tiles per row block
     int tiles, n_tiles;
-    int io;                   // boxes per epilogue warp (TMA epilogue)
+    int io;                   // boxes per stream (TMA epilogue)
 };
 
 template <int BN, bool kPair> struct Shape {
@@ -67,71 +76,91 @@ template <int BN, bool kPair> struct Shape {
     static constexpr int kStage = kRowsBytes + kW + kSfBytes * (1 + kBlocks);
     static constexpr int kSfCols = 8 + kBlocks * 8;   // TMEM columns a stage's scales take
     static constexpr int kSharedCols = kPair ? 128 : 0;
-    static constexpr int kSecond = BN - kSharedCols;  // first column of accumulator 1
-    static constexpr int kSfBase = kSecond + BN;
+    static constexpr int kSecond = BN - kSharedCols;  // from an accumulator to the next
+    static constexpr int kAccs = kPair ? 2 : 3;
+    static constexpr int kSfBase = (kAccs - 1) * kSecond + BN;
     static constexpr int kSfStages = (kTmem - kSfBase) / kSfCols;  // most ring stages
     static constexpr int kGroups = kPair ? 1 : 2;     // epilogue groups
     static constexpr int kEpiWarps = kGroups * kGroupWarps;
-    static constexpr int kThreads = 32 * (4 + kEpiWarps);
+    static constexpr int kThreads = 32 * (5 + kEpiWarps);
 };
 
 // Tail of the dynamic shared memory behind the ring and the epilogue's boxes.
 constexpr int kPatch = 32 * 33 * 4;  // an epilogue warp's transposing patch (plain epilogue)
 struct Tail {
     alignas(16) float bias[kMaxEpiWarps][64];  // read four at a time
-    unsigned long long bars[2 * 8 + 2 * 2 + 4];
-    unsigned long long r_full[kMaxEpiWarps][kMaxIo];
+    unsigned long long bars[2 * 8 + 2 * 3 + 4];
+    // by stream and slot: shortcut loaded, box written, box free again
+    unsigned long long r_full[4][kMaxIo], ready[4][kMaxIo], free_box[4][kMaxIo];
     uint32_t tmem;
     int abort_flag;
 };
 
-// The boxes of 32 rows x 128 bytes that an epilogue warp works through, in
-// order: the tiles of its group, per tile every second box (the warp's side),
-// from the columns that the accumulators share on.
-template <typename T, int BN, bool kPair> struct Boxes {
-    using S = Shape<BN, kPair>;
-    static constexpr int kCols = 128 / sizeof(T);
-    static constexpr int kPer = BN / kCols;                  // boxes per tile, both sides
-    int t, step, end, n_tiles, acc, side, row_off;
-    int j;
+// The tiles of a CTA (or of one of its epilogue groups): every `step`-th of the
+// n_tiles x m_tiles, channels first.
+struct Tiles {
+    int t, end, step, mt, nt, n_tiles, step_m, step_n;
 
-    __device__ __forceinline__ Boxes(const MxArgs &a, int unit, int units, int group, int side_,
-                                     int row_off_)
-        : t(unit + group * units), step(S::kGroups * units), end(a.tiles), n_tiles(a.n_tiles),
-          acc(group), side(side_), row_off(row_off_), j(side_)
+    __device__ __forceinline__ Tiles(const MxArgs &a, int first, int step_)
+        : t(first), end(a.tiles), step(step_), mt(first / a.n_tiles), nt(first - mt * a.n_tiles),
+          n_tiles(a.n_tiles), step_m(step_ / a.n_tiles), step_n(step_ - step_m * a.n_tiles)
     {
-        if (j >= kPer)
-            t = end;  // a side without boxes
     }
     __device__ __forceinline__ bool done() const { return t >= end; }
-    __device__ __forceinline__ bool first_of_tile() const { return j == side; }
-    __device__ __forceinline__ bool last_of_tile() const { return j + 2 >= kPer; }
-    // the warp's last box in the shared columns
-    __device__ __forceinline__ bool last_shared() const
-    {
-        return j < S::kSharedCols / kCols && j + 2 >= S::kSharedCols / kCols;
-    }
-    // first column within the tile: accumulator 0 shares its last columns with
-    // the first of accumulator 1
-    __device__ __forceinline__ int col() const { return (acc ? j : kPer - 1 - j) * kCols; }
-    __device__ __forceinline__ int channel() const { return t % n_tiles * BN + col(); }
-    __device__ __forceinline__ long long row() const
-    {
-        return static_cast<long long>(t / n_tiles) * (kPair ? 256 : 128) + row_off;
-    }
     __device__ __forceinline__ void next()
     {
-        j += 2;
-        if (j < kPer)
-            return;
-        j = side;
         t += step;
-        if (S::kGroups == 1)
-            acc ^= 1;
+        mt += step_m;
+        nt += step_n;
+        if (nt >= n_tiles) {
+            nt -= n_tiles;
+            ++mt;
+        }
     }
 };
 
-// kIo: outputs (and the shortcut) move as 32 x 128-byte boxes by TMA, which
+// The boxes of 128 rows x 128 bytes of a tile, in the order in which they are
+// worked on: from the columns that the accumulators share on (accumulator 0
+// shares its last columns with the first of accumulator 1).  Box j belongs to
+// side j & 1 of its group.
+template <typename T, int BN, bool kPair> struct Boxes {
+    static constexpr int kCols = 128 / sizeof(T);
+    static constexpr int kPer = BN / kCols;
+    static __device__ __forceinline__ int col(int acc, int j)
+    {
+        return (acc ? j : kPer - 1 - j) * kCols;
+    }
+};
+
+// Slot and phase of a stream's boxes.
+struct Slot {
+    int d = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int io)
+    {
+        if (++d == io) {
+            d = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Accumulator of a tile and the parity of its use.
+template <int kAccs> struct Turn {
+    int acc;
+    uint32_t phase = 0;
+    __device__ __forceinline__ explicit Turn(int first) : acc(first) {}
+    __device__ __forceinline__ void next(int tiles)
+    {
+        acc += tiles;
+        if (acc >= kAccs) {
+            acc -= kAccs;
+            phase ^= 1u;
+        }
+    }
+};
+
+// kIo: outputs (and the shortcut) move as 128 x 128-byte boxes by TMA, which
 // needs rows of a multiple of 16 bytes; otherwise the plain epilogue transposes
 // through shared memory and stores element by element.
 template <typename T, int BN, bool kPair, bool kIo>
@@ -144,19 +173,20 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
 {
     using S = Shape<BN, kPair>;
     extern __shared__ uint8_t raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
-                                                ~static_cast<uintptr_t>(1023));
+    // (aligned by an offset: a pointer made from an integer would lose its
+    // address space, and every access through it become a generic one)
+    uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     // the epilogue's boxes first: they keep the 1024-byte alignment of the swizzle
-    const int epi_bytes = S::kEpiWarps * (kIo ? a.io * kIoBox : kPatch);
+    const int epi_bytes = kIo ? 2 * S::kGroups * a.io * kIoBox : S::kEpiWarps * kPatch;
     const uint32_t ring = sbase + ((epi_bytes + 1023) & ~1023);
     Tail *tail = reinterpret_cast<Tail *>(smem + (ring - sbase) + a.stages * S::kStage);
     const uint32_t bars = smem_u32(tail->bars);
     const auto full = [&](int s) { return bars + 8u * s; };
     const auto empty = [&](int s) { return bars + 8u * (a.stages + s); };
     const auto acc_full = [&](int b) { return bars + 8u * (2 * a.stages + b); };
-    const auto acc_empty = [&](int b) { return bars + 8u * (2 * a.stages + 2 + b); };
-    const uint32_t mma_done = bars + 8u * (2 * a.stages + 4), never = mma_done + 8u;
+    const auto acc_empty = [&](int b) { return bars + 8u * (2 * a.stages + 3 + b); };
+    const uint32_t mma_done = bars + 8u * (2 * a.stages + 6), never = mma_done + 8u;
     const uint32_t exit_bar = never + 8u, shared_free = never + 16u;
     volatile int *abort_flag = &tail->abort_flag;
     const WaitCtl ctl{abort_flag, a.status, a.inject == 1 ? 4 * a.wait_ns : a.wait_ns};
@@ -171,14 +201,19 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        // drained by the group's warps; of a pair, rank 1's count as one at rank 0
+        const int drains = kGroupWarps + (kPair && rank == 0 ? 1 : 0);
+        for (int b = 0; b < S::kAccs; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), kGroupWarps * (kPair ? 2 : 1));
+            mbar_init(acc_empty(b), drains);
         }
-        mbar_init(shared_free, 2 * kGroupWarps);  // of both CTAs
-        for (int w = 0; w < S::kEpiWarps; ++w)
-            for (int b = 0; b < kMaxIo; ++b)
-                mbar_init(smem_u32(&tail->r_full[w][b]), 1);
+        mbar_init(shared_free, drains);
+        for (int q = 0; q < 4; ++q)
+            for (int d = 0; d < kMaxIo; ++d) {
+                mbar_init(smem_u32(&tail->r_full[q][d]), 1);
+                mbar_init(smem_u32(&tail->ready[q][d]), 4);  // a warp per lane quarter
+                mbar_init(smem_u32(&tail->free_box[q][d]), 1);
+            }
         mbar_init(mma_done, 1);
         mbar_init(never, 1);
         mbar_init(exit_bar, 1);
@@ -208,58 +243,49 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
     griddep_wait();  // from here on global memory is touched
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int t = unit; ok && t < a.tiles; t += units) {
-                const int mt = t / a.n_tiles, nt = t - mt * a.n_tiles;
-                const int n0 = nt * BN;
-                const int xblk = kPair ? 2 * mt + static_cast<int>(rank) : mt;
-                for (int k = 0; k < a.k_steps; ++k) {
-                    if (!mbar_wait(empty(s), ph ^ 1u, ctl, kDevTimeoutProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = ring + s * S::kStage, sf = st + kRowsBytes + S::kW;
-                    if constexpr (kPair) {
-                        // both CTAs' loads complete on rank 0's barrier
-                        if (rank == 0)
-                            mbar_arrive_expect_tx(full(s), 2 * S::kStage);
-                        const uint32_t bar = mapa_shared(full(s), 0);
-                        tma2_load_2d(st, &tmX, bar, k * 128, xblk * 128);
-                        tma2_load_2d(st + kRowsBytes, &tmW, bar, k * 128,
-                                     n0 + static_cast<int>(rank) * S::kWRows);
-                        tma2_load_2d(sf, &tmXs, bar, 0, xblk * a.kt + 2 * k);
-#pragma unroll
-                        for (int j = 0; j < S::kBlocks; ++j)
-                            tma2_load_2d(sf + kSfBytes * (1 + j), &tmWs, bar, 0,
-                                         (n0 / 128 + j) * a.kt + 2 * k);
-                    } else {
-                        mbar_arrive_expect_tx(full(s), S::kStage);
-                        tma_load_2d(st, &tmX, full(s), k * 128, xblk * 128);
-                        tma_load_2d(st + kRowsBytes, &tmW, full(s), k * 128, n0);
-                        tma_load_2d(sf, &tmXs, full(s), 0, xblk * a.kt + 2 * k);
-#pragma unroll
-                        for (int j = 0; j < S::kBlocks; ++j)
-                            tma_load_2d(sf + kSfBytes * (1 + j), &tmWs, full(s), 0,
-                                        (n0 / 128 + j) * a.kt + 2 * k);
-                    }
-                    ++issued;
-                    if (++s == a.stages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = lane == 0;
+        for (Tiles t(a, unit, units); ok && !t.done(); t.next()) {
+            const int n0 = t.nt * BN;
+            const int xblk = kPair ? 2 * t.mt + static_cast<int>(rank) : t.mt;
+            for (int k = 0; k < a.k_steps; ++k) {
+                if (!mbar_wait(empty(s), ph ^ 1u, ctl, kDevTimeoutProducer)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t st = ring + s * S::kStage, sf = st + kRowsBytes + S::kW;
+                if constexpr (kPair) {
+                    // both CTAs' loads complete on rank 0's barrier
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(full(s), 2 * S::kStage);
+                    const uint32_t bar = mapa_shared(full(s), 0);
+                    tma2_load_2d(st, &tmX, bar, k * 128, xblk * 128);
+                    tma2_load_2d(st + kRowsBytes, &tmW, bar, k * 128,
+                                 n0 + static_cast<int>(rank) * S::kWRows);
+                    tma2_load_3d(sf, &tmXs, bar, 0, 2 * k, xblk);
+                    tma2_load_3d(sf + kSfBytes, &tmWs, bar, 0, 2 * k, n0 / 128);
+                } else {
+                    mbar_arrive_expect_tx(full(s), S::kStage);
+                    tma_load_2d(st, &tmX, full(s), k * 128, xblk * 128);
+                    tma_load_2d(st + kRowsBytes, &tmW, full(s), k * 128, n0);
+                    tma_load_3d(sf, &tmXs, full(s), 0, 2 * k, xblk);
+                    tma_load_3d(sf + kSfBytes, &tmWs, full(s), 0, 2 * k, n0 / 128);
+                }
+                ++issued;
+                if (++s == a.stages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            // Let every copy still in flight land (after a failed wait elsewhere
-            // nobody else waited for the last ones).  Of a pair, rank 0 waits for
-            // both and the exit handshake holds rank 1 until then.
-            if (rank == 0)
-                for (int i = max(0, issued - a.stages); i < issued; ++i)
-                    if (!mbar_drain(full(i % a.stages), (i / a.stages) & 1, kDrainNs))
-                        atomicOr(a.status, kDevDrainFailed);
         }
+        // Let every copy still in flight land (after a failed wait elsewhere nobody
+        // else waited for the last ones).  Of a pair, rank 0 waits for both and the
+        // exit handshake holds rank 1 until then.
+        if (rank == 0 && lane == 0)
+            for (int i = max(0, issued - a.stages); i < issued; ++i)
+                if (!mbar_drain(full(i % a.stages), (i / a.stages) & 1, kDrainNs))
+                    atomicOr(a.status, kDevDrainFailed);
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         bool ok = true;
@@ -279,16 +305,17 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
         };
         int s = 0, i = 0;
         uint32_t ph = 0;
-        for (int t = unit; ok && t < a.tiles; t += units, ++i) {
+        Turn<S::kAccs> turn(0);
+        for (Tiles t(a, unit, units); ok && !t.done(); t.next(), turn.next(1), ++i) {
             // The accumulator is free: its own last tile is drained, and the tile
             // before this one has left the shared columns.
-            if (!wait(acc_empty(i & 1), ((i >> 1) & 1) ^ 1) ||
+            if (!wait(acc_empty(turn.acc), turn.phase ^ 1u) ||
                 (kPair && i > 0 && !wait(shared_free, (i - 1) & 1)))
                 break;
             tc_fence_after();
-            const uint32_t d = tmem + (i & 1) * S::kSecond;
+            const uint32_t d = tmem + turn.acc * S::kSecond;
             // BN = 64: the tile's scales are the lower or upper half of a 128-row block
-            const uint32_t half = BN == 64 ? ((t % a.n_tiles) & 1) * 2u : 0u;
+            const uint32_t half = BN == 64 ? (t.nt & 1) * 2u : 0u;
             for (int k = 0; k < a.k_steps; ++k) {
                 if (!wait(full(s), ph)) {
                     ok = false;
@@ -301,9 +328,13 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
                 constexpr uint32_t kM = kPair ? 256 : 128;
                 const int left = (a.K - k * kStageK + 63) / 64;  // K = 64 steps
                 if (left >= 4) {
-                    mma_mx4_stage<kPair, S::kBlocks>(d, ad, bd, idesc_mx4(kM, BN, 0),
-                                                     idesc_mx4(kM, BN, 2), sfa, sfw, half,
-                                                     smem_desc_scales(sf), k > 0);
+                    mma_mx4_stage<kPair, S::kBlocks, 4>(d, ad, bd, idesc_mx4(kM, BN, 0),
+                                                        idesc_mx4(kM, BN, 2), sfa, sfw, half,
+                                                        smem_desc_scales(sf), k > 0);
+                } else if (left == 2) {
+                    mma_mx4_stage<kPair, S::kBlocks, 2>(d, ad, bd, idesc_mx4(kM, BN, 0),
+                                                        idesc_mx4(kM, BN, 2), sfa, sfw, half,
+                                                        smem_desc_scales(sf), k > 0);
                 } else {
                     for (int j = 0; j < (left + 1) / 2; ++j) {
                         tmem_cp_scales<kPair>(sfa + 4 * j, smem_desc_scales(sf + 512 * j));
@@ -326,12 +357,103 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
             }
             if (!ok)
                 break;
-            commit(acc_full(i & 1));
+            commit(acc_full(turn.acc));
         }
         // No MMA may still read shared memory or write TMEM behind this point.
         commit(mma_done);
         if (lane == 0 && !mbar_drain(mma_done, 0, kDrainNs))
             atomicOr(a.status, kDevDrainFailed);
+        __syncwarp();
+    } else if (kPair && warp == 1) {
+        // ---- rank 1: its epilogue's hand-backs, passed on in tile order -------------
+        if (lane == 0) {
+            Turn<S::kAccs> turn(0);
+            int i = 0;
+            for (Tiles t(a, unit, units); !t.done(); t.next(), turn.next(1), ++i) {
+                if (!mbar_wait(shared_free, i & 1, ctl, kDevTimeoutMma))
+                    break;
+                mbar_arrive_cluster(mapa_shared(shared_free, 0));
+                if (!mbar_wait(acc_empty(turn.acc), turn.phase, ctl, kDevTimeoutMma))
+                    break;
+                mbar_arrive_cluster(mapa_shared(acc_empty(turn.acc), 0));
+            }
+        }
+        __syncwarp();
+    } else if (kIo && warp == 2) {
+        // ---- shortcut loads, boxes in tile order ------------------------------------
+        using B = Boxes<T, BN, kPair>;
+        if (lane == 0 && a.r) {
+            Slot slot[S::kGroups][2];
+            int group = 0;
+            bool ok = true;
+            Turn<S::kAccs> turn(0);
+            for (Tiles t(a, unit, units); ok && !t.done(); t.next(), turn.next(1)) {
+                const int row = t.mt * (kPair ? 256 : 128) + static_cast<int>(rank) * 128;
+#pragma unroll
+                for (int j = 0; j < B::kPer; ++j) {
+                    Slot &sl = S::kGroups == 2 && group ? slot[S::kGroups - 1][j & 1] : slot[0][j & 1];
+                    const int q = group * 2 + (j & 1);
+                    const int ch = t.nt * BN + B::col(turn.acc, j);
+                    const uint32_t bar = smem_u32(&tail->r_full[q][sl.d]);
+                    if (!mbar_wait(smem_u32(&tail->free_box[q][sl.d]), sl.phase ^ 1u, ctl,
+                                   kDevTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    if (row < a.M && ch < a.N) {
+                        mbar_arrive_expect_tx(bar, kIoBox);
+                        tma_load_2d(sbase + (q * a.io + sl.d) * kIoBox, &tmR, bar, ch, row);
+                    } else {
+                        mbar_arrive(bar);
+                    }
+                    sl.next(a.io);
+                }
+                group ^= S::kGroups - 1;
+            }
+            // Shortcut boxes in flight land before the CTA leaves: the last load of
+            // slot d was in the stream's current phase if d lies before its next slot.
+#pragma unroll
+            for (int q = 0; q < 2 * S::kGroups; ++q) {
+                const Slot &sl = slot[q / 2][q & 1];
+                for (int d = 0; d < a.io; ++d)
+                    if (!mbar_drain(smem_u32(&tail->r_full[q][d]),
+                                    d < sl.d ? sl.phase : sl.phase ^ 1u, kDrainNs))
+                        atomicOr(a.status, kDevDrainFailed);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 3 || warp == 4 + S::kEpiWarps) {
+        // ---- stores of one side's boxes, in tile order ------------------------------
+        using B = Boxes<T, BN, kPair>;
+        const int side = warp == 3 ? 0 : 1;
+        if (kIo && lane == 0 && side < B::kPer) {
+            Slot slot[S::kGroups];
+            int group = 0;
+            bool ok = true;
+            Turn<S::kAccs> turn(0);
+            for (Tiles t(a, unit, units); ok && !t.done(); t.next(), turn.next(1)) {
+                const int row = t.mt * (kPair ? 256 : 128) + static_cast<int>(rank) * 128;
+                Slot &sl = S::kGroups == 2 && group ? slot[S::kGroups - 1] : slot[0];
+                const int q = group * 2 + side;
+                for (int j = side; j < B::kPer; j += 2) {
+                    const int ch = t.nt * BN + B::col(turn.acc, j);
+                    if (!mbar_wait(smem_u32(&tail->ready[q][sl.d]), sl.phase, ctl,
+                                   kDevTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    if (row < a.M && ch < a.N) {
+                        tma_store_2d(&tmO, sbase + (q * a.io + sl.d) * kIoBox, ch, row);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                    }
+                    mbar_arrive(smem_u32(&tail->free_box[q][sl.d]));
+                    sl.next(a.io);
+                }
+                group ^= S::kGroups - 1;
+            }
+            bulk_wait_all();
+        }
         __syncwarp();
     } else if (warp >= 4) {
         const int e = warp - 4, quarter = e & 3, side = (e >> 2) & 1, group = e >> 3;
@@ -340,190 +462,145 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
         const auto release = [&](uint32_t bar) {  // after the warp's reads of the accumulator
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if (kPair)
-                    mbar_arrive_cluster(mapa_shared(bar, 0));
-                else
-                    mbar_arrive(bar);
-            }
+            if (lane == 0)
+                mbar_arrive(bar);
         };
-        uint32_t acc_phase = 0;  // parity per accumulator, one bit each
-        const auto wait_acc = [&](int acc) {
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full(acc), (acc_phase >> acc) & 1,
-                                                              ctl, kDevTimeoutEpilogue));
-            acc_phase ^= 1u << acc;
+        Turn<S::kAccs> turn(group);
+        const auto wait_acc = [&]() {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full(turn.acc), turn.phase, ctl,
+                                                              kDevTimeoutEpilogue));
             tc_fence_after();
             return ok;
         };
         if constexpr (kIo) {
             using B = Boxes<T, BN, kPair>;
-            const uint32_t boxes = sbase + e * a.io * kIoBox;
-            uint8_t *boxes_p = smem + e * a.io * kIoBox;
+            const int q = group * 2 + side;  // the stream
             float *bias = tail->bias[e];
-            const uint32_t r_full = smem_u32(tail->r_full[e]);
-            B cur(a, unit, units, group, side, row_off), ahead = cur;
-            int n_ahead = 0;  // shortcut boxes asked for so far
-            const auto ask = [&](int most) {
-                // ask for shortcut boxes up to (not including) number `most`
-                for (; n_ahead < most && !ahead.done(); ++n_ahead, ahead.next()) {
-                    if (lane == 0 && ahead.row() < a.M && ahead.channel() < a.N) {
-                        const int d = a.io == 2 ? n_ahead & 1 : 0;
-                        mbar_arrive_expect_tx(r_full + 8 * d, kIoBox);
-                        tma_load_2d(boxes + d * kIoBox, &tmR, r_full + 8 * d, ahead.channel(),
-                                    static_cast<int>(ahead.row()));
-                    }
-                }
-            };
-            uint32_t r_phase = 0;  // parity per box slot, one bit each
+            Slot slot;
             // a box's bias is loaded one box ahead, two channels a lane
             float b0 = 0.f, b1 = 0.f;
-            const auto load_bias = [&](const B &at) {
-                if (a.bias && !at.done()) {
-                    const int c = at.channel() + lane;
+            const auto load_bias = [&](int c) {
+                if (a.bias) {
+                    c += lane;
                     b0 = c < a.N ? __ldg(a.bias + c) : 0.f;
                     if (B::kCols == 64)
                         b1 = c + 32 < a.N ? __ldg(a.bias + c + 32) : 0.f;
                 }
             };
-            load_bias(cur);
-            int i = 0;
+            Tiles t(a, unit + group * units, S::kGroups * units);
+            if (!t.done())
+                load_bias(t.nt * BN + B::col(turn.acc, side));
             bool ok = true;
-            B now = cur;
-            for (; !cur.done(); ++i) {
-                now = cur;
-                cur.next();
-                const int d = a.io == 2 ? i & 1 : 0;
-                const int ch = now.channel();
-                const long long row = now.row();
-                const bool inside = row < a.M && ch < a.N;
-                // A slot is free once its last store has read it.
-                if (lane == 0) {
-                    if (a.r || a.io == 1)
-                        bulk_wait_read<0>();
-                    else
-                        bulk_wait_read<1>();
-                }
-                if (a.r) {
-                    __syncwarp();
-                    ask(i + a.io);
-                }
-                if (now.first_of_tile() && !wait_acc(now.acc)) {
-                    ok = false;
+            while (ok && !t.done()) {
+                if (!wait_acc())
                     break;
-                }
-                if (a.r && inside) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(r_full + 8 * d, (r_phase >> d) & 1, ctl,
-                                                           kDevTimeoutEpilogue))) {
+                const int acc = turn.acc, n0 = t.nt * BN;
+                t.next();
+                turn.next(S::kGroups);
+                const int n0_next = t.done() ? 0 : t.nt * BN;
+                for (int j = side; j < B::kPer; j += 2) {
+                    // The box is free, or holds the shortcut.
+                    const uint32_t bar = smem_u32(a.r ? &tail->r_full[q][slot.d]
+                                                      : &tail->free_box[q][slot.d]);
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(bar, a.r ? slot.phase : slot.phase ^ 1u, ctl,
+                                              kDevTimeoutEpilogue))) {
                         ok = false;
                         break;
                     }
-                    r_phase ^= 1u << d;
-                }
-                // Pair: the box's columns are read at once, and the accumulator (or
-                // its shared part) handed back before the arithmetic.  One CTA with
-                // two groups has the registers for 32 columns at a time.
-                const uint32_t acc = lanes_at + now.acc * S::kSecond + now.col();
-                uint32_t v[kPair ? B::kCols / 32 : 1][32];
-                if constexpr (kPair) {
+                    // Pair: the box's columns are read at once, and the accumulator (or
+                    // its shared part) handed back before the arithmetic.  One CTA with
+                    // two groups has the registers for 32 columns at a time.
+                    const uint32_t at_acc = lanes_at + acc * S::kSecond + B::col(acc, j);
+                    uint32_t v[kPair ? B::kCols / 32 : 1][32];
+                    if constexpr (kPair) {
 #pragma unroll
-                    for (int h = 0; h < B::kCols / 32; ++h)
-                        tmem_ld_32x32b_x32(acc + 32 * h, v[h]);
-                }
-                bias[lane] = b0;
-                if (B::kCols == 64)
-                    bias[32 + lane] = b1;
-                load_bias(cur);
-                if constexpr (kPair) {
-#pragma unroll
-                    for (int h = 0; h < B::kCols / 32; ++h)
-                        tmem_ld_wait(v[h]);
-                    if (now.last_shared())
-                        release(shared_free);
-                    if (now.last_of_tile())
-                        release(acc_empty(now.acc));
-                }
-                __syncwarp();
-                uint8_t *mine = boxes_p + d * kIoBox + lane * 128;
-#pragma unroll
-                for (int h = 0; h < B::kCols / 32; ++h) {
-                    if constexpr (!kPair)
-                        tmem_ld_32x32b_x32_sync(acc + 32 * h, v[0]);
-                    const uint32_t(&w)[32] = v[kPair ? h : 0];
-                    // 16 bytes (kV elements) at a time
-                    constexpr int kV = 16 / sizeof(T);
-#pragma unroll
-                    for (int c = 0; c < 32; c += kV) {
-                        uint8_t *at = mine + ((((32 * h + c) / kV) ^ (lane & 7)) * 16);
-                        F2 f[kV / 2];
-#pragma unroll
-                        for (int j = 0; j < kV; j += 4) {
-                            const float4 b = *reinterpret_cast<const float4 *>(bias + 32 * h + c + j);
-                            f[j / 2] = add2(f2(__uint_as_float(w[c + j]), __uint_as_float(w[c + j + 1])),
-                                            f2(b.x, b.y));
-                            f[j / 2 + 1] = add2(f2(__uint_as_float(w[c + j + 2]),
-                                                   __uint_as_float(w[c + j + 3])),
-                                                f2(b.z, b.w));
-                        }
-                        if (a.r) {
-                            const Vec<T, kV> rv = *reinterpret_cast<const Vec<T, kV> *>(at);
-                            F2 g[kV / 2];
-                            unpack<T, kV>(rv, g);
-#pragma unroll
-                            for (int j = 0; j < kV / 2; ++j)
-                                f[j] = add2(f[j], g[j]);
-                        }
-                        store_vec<T, kV>(reinterpret_cast<T *>(at), finish<T, kV>(f, a.act));
+                        for (int h = 0; h < B::kCols / 32; ++h)
+                            tmem_ld_32x32b_x32(at_acc + 32 * h, v[h]);
                     }
-                }
-                if (!kPair && now.last_of_tile())
-                    release(acc_empty(now.acc));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (inside)
-                        tma_store_2d(&tmO, boxes + d * kIoBox, ch, static_cast<int>(row));
-                    bulk_commit();
-                }
-            }
-            // Shortcut boxes asked for but not used land before the CTA leaves.
-            if (a.r && !ok && lane == 0) {
-                for (int k = i; k < n_ahead && !now.done(); ++k, now.next()) {
-                    const int d = a.io == 2 ? k & 1 : 0;
-                    if (now.row() < a.M && now.channel() < a.N) {
-                        if (!mbar_drain(r_full + 8 * d, (r_phase >> d) & 1, kDrainNs))
-                            atomicOr(a.status, kDevDrainFailed);
+                    bias[lane] = b0;
+                    if (B::kCols == 64)
+                        bias[32 + lane] = b1;
+                    const bool last = j + 2 >= B::kPer;
+                    load_bias(last ? n0_next + B::col(turn.acc, side) : n0 + B::col(acc, j + 2));
+                    if constexpr (kPair) {
+#pragma unroll
+                        for (int h = 0; h < B::kCols / 32; ++h)
+                            tmem_ld_wait(v[h]);
+                        constexpr int kShared = S::kSharedCols / B::kCols;
+                        if (j < kShared && j + 2 >= kShared)
+                            release(shared_free);
+                        if (last)
+                            release(acc_empty(acc));
                     }
+                    __syncwarp();
+                    uint8_t *mine = smem + (q * a.io + slot.d) * kIoBox + (quarter * 32 + lane) * 128;
+#pragma unroll
+                    for (int h = 0; h < B::kCols / 32; ++h) {
+                        if constexpr (!kPair)
+                            tmem_ld_32x32b_x32_sync(at_acc + 32 * h, v[0]);
+                        const uint32_t(&w)[32] = v[kPair ? h : 0];
+                        // 16 bytes (kV elements) at a time
+                        constexpr int kV = 16 / sizeof(T);
+#pragma unroll
+                        for (int c = 0; c < 32; c += kV) {
+                            uint8_t *at = mine + ((((32 * h + c) / kV) ^ (lane & 7)) * 16);
+                            F2 f[kV / 2];
+#pragma unroll
+                            for (int i = 0; i < kV; i += 4) {
+                                const float4 b =
+                                    *reinterpret_cast<const float4 *>(bias + 32 * h + c + i);
+                                f[i / 2] = add2(f2(__uint_as_float(w[c + i]),
+                                                   __uint_as_float(w[c + i + 1])),
+                                                f2(b.x, b.y));
+                                f[i / 2 + 1] = add2(f2(__uint_as_float(w[c + i + 2]),
+                                                       __uint_as_float(w[c + i + 3])),
+                                                    f2(b.z, b.w));
+                            }
+                            if (a.r) {
+                                const Vec<T, kV> rv = *reinterpret_cast<const Vec<T, kV> *>(at);
+                                F2 g[kV / 2];
+                                unpack<T, kV>(rv, g);
+#pragma unroll
+                                for (int i = 0; i < kV / 2; ++i)
+                                    f[i] = add2(f[i], g[i]);
+                            }
+                            store_vec<T, kV>(reinterpret_cast<T *>(at), finish<T, kV>(f, a.act));
+                        }
+                    }
+                    if (!kPair && last)
+                        release(acc_empty(acc));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&tail->ready[q][slot.d]));
+                    slot.next(a.io);
                 }
-            }
-            if (side >= B::kPer) {
-                // this side has no boxes: it still answers for its share of the barrier
+                // a side without boxes still answers for its share of the barriers
                 // (only a 64-channel tile of one CTA: no shared columns)
-                for (int t = unit + group * units; t < a.tiles && wait_acc(group); t += 2 * units)
-                    release(acc_empty(group));
+                if (side >= B::kPer)
+                    release(acc_empty(acc));
             }
-            if (lane == 0)
-                bulk_wait_all();
         } else {
             float *patch = reinterpret_cast<float *>(smem) + e * (kPatch / 4);
             constexpr int kParts = BN / 64;  // of 64 columns, 32 for each side
-            int acc = group;
-            for (int t = unit + group * units; t < a.tiles && wait_acc(acc);
-                 t += S::kGroups * units) {
-                const int mt = t / a.n_tiles, nt = t - mt * a.n_tiles;
-                const long long row0 = static_cast<long long>(mt) * (kPair ? 256 : 128) + row_off;
+            for (Tiles t(a, unit + group * units, S::kGroups * units); !t.done() && wait_acc();
+                 t.next(), turn.next(S::kGroups)) {
+                const int acc = turn.acc;
+                const long long row0 = static_cast<long long>(t.mt) * (kPair ? 256 : 128) + row_off;
                 const int rows = static_cast<int>(max(0ll, min(32ll, a.M - row0)));
                 for (int part = 0; part < kParts; ++part) {
                     // the shared columns first
                     const int c0 = (acc ? part : kParts - 1 - part) * 64 + side * 32;
                     uint32_t v[32];
                     tmem_ld_32x32b_x32_sync(lanes_at + acc * S::kSecond + c0, v);
-                    if (part == S::kSharedCols / 64 - 1)
+                    if (kPair && part == S::kSharedCols / 64 - 1)
                         release(shared_free);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         patch[lane * 33 + i] = __uint_as_float(v[i]);
                     __syncwarp();
-                    const int o = nt * BN + c0 + lane;
+                    const int o = t.nt * BN + c0 + lane;
                     if (o < a.N) {
                         const float b = a.bias ? a.bias[o] : 0.f;
                         size_t at = static_cast<size_t>(row0) * a.N + o;
@@ -538,8 +615,6 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
                     __syncwarp();
                 }
                 release(acc_empty(acc));
-                if (S::kGroups == 1)
-                    acc ^= 1;
             }
         }
         __syncwarp();
@@ -597,12 +672,8 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
     if (tiles > 0x7fffffffLL)
         return X1CB_ERR_SHAPE;
     a.tiles = static_cast<int>(tiles);
-    // With a shortcut and a short K two boxes per epilogue warp: the next shortcut
-    // box arrives beside the current one (200704 x 128 x 512: 79.9 us, with one box
-    // 84.1).  Otherwise one: a deeper ring is worth more (200704 x 512 x 128 without
-    // a shortcut 23.3 us, with two boxes 29.6).
-    a.io = !kPair && c.r && a.k_steps <= 2 ? 2 : 1;
-    const int epi = (S::kEpiWarps * (kIo ? a.io * kIoBox : kPatch) + 1023) & ~1023;
+    a.io = kPair ? (a.k_steps >= 12 ? 1 : 2) : c.r && a.k_steps <= 2 ? 2 : 1;
+    const int epi = ((kIo ? 2 * S::kGroups * a.io * kIoBox : S::kEpiWarps * kPatch) + 1023) & ~1023;
     const int fixed = 1024 + epi + static_cast<int>(sizeof(Tail));
     a.stages = std::min({(232448 - fixed) / S::kStage, S::kSfStages, 8});
     const int smem = fixed + a.stages * S::kStage;
@@ -616,22 +687,22 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
         return e;
     if (int e = encode_map(&tmW, c.w, 2, dw, str, bw, CU_TENSOR_MAP_SWIZZLE_128B))
         return e;
-    // scales as rows of one tile (128 words), two tiles to a box
-    const uint64_t sstr[1] = {512};
-    const uint64_t dxs[2] = {128, static_cast<uint64_t>((c.M + 127) / 128) * a.kt};
-    const uint64_t dws[2] = {128, static_cast<uint64_t>((c.N + 127) / 128) * a.kt};
-    const uint32_t bs[2] = {128, 2};
-    if (int e = encode_map(&tmXs, c.xs, 2, dxs, sstr, bs, CU_TENSOR_MAP_SWIZZLE_NONE,
+    // scales: tiles of 128 words, kt of them per block of 128 rows
+    const uint64_t sstr[2] = {512, static_cast<uint64_t>(a.kt) * 512};
+    const uint64_t dxs[3] = {128, static_cast<uint64_t>(a.kt), static_cast<uint64_t>((c.M + 127) / 128)};
+    const uint64_t dws[3] = {128, static_cast<uint64_t>(a.kt), static_cast<uint64_t>((c.N + 127) / 128)};
+    const uint32_t bxs[3] = {128, 2, 1}, bws[3] = {128, 2, S::kBlocks};
+    if (int e = encode_map(&tmXs, c.xs, 3, dxs, sstr, bxs, CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_DATA_TYPE_UINT32))
         return e;
-    if (int e = encode_map(&tmWs, c.ws, 2, dws, sstr, bs, CU_TENSOR_MAP_SWIZZLE_NONE,
+    if (int e = encode_map(&tmWs, c.ws, 3, dws, sstr, bws, CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_DATA_TYPE_UINT32))
         return e;
     tmR = tmO = tmX;  // unused without kIo
     if (kIo) {
         const uint64_t ostr[1] = {static_cast<uint64_t>(c.N) * sizeof(T)};
         const uint64_t d[2] = {static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.M)};
-        const uint32_t b[2] = {128 / sizeof(T), 32};
+        const uint32_t b[2] = {128 / sizeof(T), 128};
         if (int e = encode_map(&tmO, c.out, 2, d, ostr, b, CU_TENSOR_MAP_SWIZZLE_128B,
                                map_type(c.dtype)))
             return e;

@@ -830,53 +830,83 @@ __device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_
             : "memory");
 }
 
-// A whole ring stage of K = 256 in one go: the scale copies of both K = 128
-// halves (one tile of A, BLOCKS tiles of B each) and the four MMA steps, issued
-// by one elected lane.  sfa / sfb: the stage's scale columns; sd: descriptor of
-// its first scale tile (A's two tiles, then two per block of B; 512 bytes each);
-// sb_off: added to the scale columns of B in the MMAs.  As single wrappers, with
-// an election and operand set-up each, the ten instructions took twice the time
-// of the MMAs themselves.
-template <bool kPair, int BLOCKS>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar,
+                                            int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap *m,
+                                             uint32_t cluster_bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(cluster_bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// A ring stage of K = 256 (kSteps = 4) or its first K = 128 (kSteps = 2) in one
+// go: the scale copies of each K = 128 half (one tile of A, BLOCKS tiles of B)
+// and the MMA steps, issued by one elected lane.  sfa / sfb: the stage's scale
+// columns; sd: descriptor of its first scale tile (A's two tiles, then two per
+// block of B; 512 bytes each); sb_off: added to the scale columns of B in the
+// MMAs.  As single wrappers, with an election and operand set-up each, the ten
+// instructions took twice the time of the MMAs themselves.
+template <bool kPair, int BLOCKS, int kSteps>
 __device__ __forceinline__ void mma_mx4_stage(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                               uint32_t idesc0, uint32_t idesc2, uint32_t sfa,
                                               uint32_t sfb, uint32_t sb_off, uint64_t sd,
                                               uint32_t accumulate)
 {
-#define X1CB_MX4_STAGE(CG, CPB)                                                                   \
+#define X1CB_CP(CG, COL, TILE)                                                                    \
+    "add.s64 s, %8, " TILE ";\n\tadd.u32 u, %6, " COL ";\n\t"                                     \
+    "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [u], s;\n\t"
+#define X1CB_CP2(CG)                                                                              \
+    "add.s64 s, %8, 32;\n\tadd.u32 t, %5, 4;\n\t"                                                \
+    "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [t], s;\n\t"
+#define X1CB_MMA2(CG)                                                                             \
+    "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\tadd.u32 v, u, %10;\n\t"                          \
+    "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, "      \
+    "[t], [v], q;\n\t"                                                                            \
+    "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"                                                 \
+    "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, "      \
+    "[t], [v], q;\n\t"
+#define X1CB_MX4_STAGE(CG, CPB, SECOND)                                                           \
     asm volatile(                                                                                 \
         "{\n\t.reg .pred p, q, e;\n\t.reg .b64 s, a, b;\n\t.reg .b32 t, u, v;\n\t"                  \
         "elect.sync _|e, 0xffffffff;\n\t"                                                         \
         "setp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"                                      \
-        "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [%5], %8;\n\t"                            \
-        "add.s64 s, %8, 32;\n\tadd.u32 t, %5, 4;\n\t"                                            \
-        "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [t], s;\n\t" CPB                           \
+        "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [%5], %8;\n\t" CPB                        \
         "add.u32 u, %6, %7;\n\t"                                                                  \
         "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "  \
         "[%5], [u], p;\n\t"                                                                       \
         "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"                                             \
         "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, "    \
-        "[%5], [u], q;\n\t"                                                                       \
-        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\tadd.u32 v, u, %10;\n\t"                      \
-        "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, "    \
-        "[t], [v], q;\n\t"                                                                        \
-        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"                                             \
-        "@e tcgen05.mma.cta_group::" CG ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, "    \
-        "[t], [v], q;\n\t}" ::"r"(d_tmem),                                                        \
+        "[%5], [u], q;\n\t" SECOND "}" ::"r"(d_tmem),                                             \
         "l"(adesc), "l"(bdesc), "r"(idesc0), "r"(idesc2), "r"(sfa), "r"(sfb), "r"(sb_off),        \
         "l"(sd), "r"(accumulate), "n"(BLOCKS * 4)                                                 \
         : "memory")
-#define X1CB_CP(CG, COL, TILE)                                                                    \
-    "add.s64 s, %8, " TILE ";\n\tadd.u32 u, %6, " COL ";\n\t"                                     \
-    "@e tcgen05.cp.cta_group::" CG ".32x128b.warpx4 [u], s;\n\t"
-    if constexpr (kPair) {
-        static_assert(!kPair || BLOCKS == 2, "");
-        X1CB_MX4_STAGE("2", X1CB_CP("2", "0", "64") X1CB_CP("2", "4", "128")
-                                X1CB_CP("2", "8", "96") X1CB_CP("2", "12", "160"));
-    } else {
-        X1CB_MX4_STAGE("1", X1CB_CP("1", "0", "64") X1CB_CP("1", "4", "96"));
-    }
+    static_assert(BLOCKS == (kPair ? 2 : 1), "scale blocks of 256 or up to 128 channels");
+    if constexpr (kPair && kSteps == 4)
+        X1CB_MX4_STAGE("2",
+                       X1CB_CP2("2") X1CB_CP("2", "0", "64") X1CB_CP("2", "4", "128")
+                           X1CB_CP("2", "8", "96") X1CB_CP("2", "12", "160"),
+                       X1CB_MMA2("2"));
+    else if constexpr (kPair)
+        X1CB_MX4_STAGE("2", X1CB_CP("2", "0", "64") X1CB_CP("2", "4", "128"), "");
+    else if constexpr (kSteps == 4)
+        X1CB_MX4_STAGE("1", X1CB_CP2("1") X1CB_CP("1", "0", "64") X1CB_CP("1", "4", "96"),
+                       X1CB_MMA2("1"));
+    else
+        X1CB_MX4_STAGE("1", X1CB_CP("1", "0", "64"), "");
 #undef X1CB_CP
+#undef X1CB_CP2
+#undef X1CB_MMA2
 #undef X1CB_MX4_STAGE
 }
 
