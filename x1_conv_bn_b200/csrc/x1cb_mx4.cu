@@ -1,5 +1,5 @@
 // MX4 (OCP MXFP4: e2m1 elements, one e8m0 scale per 32) conversions, and the
-// MX4 1x1 convolution in its plainest form: a warp per output channel.
+// MX4 1x1 convolution of a single row.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -97,64 +97,82 @@ __global__ void __launch_bounds__(kBlock)
     }
 }
 
-// out[m, o] for one o per warp and kRows rows m at a time.  A lane takes the
-// blocks lane, lane + 32, ... of the row: 32 products of e2m1 values, summed in
-// half precision by fours (multiples of 1/4 up to 4 * 36 = 144: exact), then
-// scaled and summed in 32 bits.
-constexpr int kRows = 4;
-template <typename T>
-__global__ void __launch_bounds__(kBlock) conv_rows_kernel(Mx4Call c)
+// The product of a single row: a warp takes kCh channels, its lanes the blocks
+// lane, lane + 32, ... of the row, four of them with all loads in flight at
+// once.  A block's 32 products of e2m1 values are summed in half precision, eight
+// to a sum (multiples of 1/4 up to 8 * 36 = 288: exact), then scaled and summed
+// in 32 bits.  Bound by latency (a launch and one trip to memory for weights that
+// fit L2 many times over): KKK.
+template <typename T, int kCh>
+__global__ void __launch_bounds__(kBlock) conv_row_kernel(Mx4Call c)
 {
-    griddep_wait();
-    const int o = blockIdx.x * (kBlock / 32) + threadIdx.x / 32;
+    constexpr int kDeep = 4;
     const int lane = threadIdx.x & 31;
-    if (o >= c.N)
+    const int o0 = (blockIdx.x * (kBlock / 32) + threadIdx.x / 32) * kCh;
+    griddep_wait();
+    if (o0 >= c.N)
         return;
     const int blocks = c.K / 32, kt = (c.K + 127) / 128;
-    const uint4 *w = reinterpret_cast<const uint4 *>(c.w) + static_cast<size_t>(o) * blocks;
-    for (long long m0 = static_cast<long long>(blockIdx.y) * kRows; m0 < c.M;
-         m0 += static_cast<long long>(gridDim.y) * kRows) {
-        float acc[kRows] = {};
-        for (int b = lane; b < blocks; b += 32) {
-            const uint4 wq = w[b];
-            const float wscale = mx4_scale_value(c.ws[mx4_scale_at(o, b, kt)]);
+    const uint4 *x = reinterpret_cast<const uint4 *>(c.x);
+    float acc[kCh] = {};
+    for (int b0 = lane; b0 < blocks; b0 += 32 * kDeep) {
+        uint4 xq[kDeep], wq[kDeep][kCh];
+        uint32_t xs[kDeep], ws[kDeep][kCh];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const long long m = m0 + r;
-                if (m >= c.M)
-                    break;
-                const uint4 xq = reinterpret_cast<const uint4 *>(c.x)[m * blocks + b];
-                const float xscale = mx4_scale_value(c.xs[mx4_scale_at(m, b, kt)]);
-                const uint32_t wa[4] = {wq.x, wq.y, wq.z, wq.w}, xa[4] = {xq.x, xq.y, xq.z, xq.w};
-                float dot = 0.f;
+        for (int d = 0; d < kDeep; ++d) {
+            const int b = b0 + 32 * d;
+            if (b < blocks) {
+                xq[d] = __ldg(x + b);
+                xs[d] = __ldg(c.xs + mx4_scale_at(0, b, kt));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    __half2 wh[4], xh[4];
-                    e2m1_to_half(wa[i], wh);
-                    e2m1_to_half(xa[i], xh);
-                    __half2 d = __hmul2(wh[0], xh[0]);
-#pragma unroll
-                    for (int j = 1; j < 4; ++j)
-                        d = __hfma2(wh[j], xh[j], d);
-                    const float2 f = __half22float2(d);
-                    dot += f.x + f.y;
+                for (int h = 0; h < kCh; ++h) {
+                    const int o = min(o0 + h, c.N - 1);
+                    wq[d][h] = __ldg(reinterpret_cast<const uint4 *>(c.w) +
+                                     static_cast<size_t>(o) * blocks + b);
+                    ws[d][h] = __ldg(c.ws + mx4_scale_at(o, b, kt));
                 }
-                acc[r] = fmaf(dot * wscale, xscale, acc[r]);
             }
         }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int d = 0; d < kDeep; ++d) {
+            if (b0 + 32 * d < blocks) {
+                const uint32_t xa[4] = {xq[d].x, xq[d].y, xq[d].z, xq[d].w};
+                __half2 xh[4][4];
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-                acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], d);
-            const long long m = m0 + r;
-            if (lane == r && m < c.M) {
-                float v = acc[r] + (c.bias ? c.bias[o] : 0.f);
-                const size_t at = static_cast<size_t>(m) * c.N + o;
-                if (c.r)
-                    v += to_f(static_cast<const T *>(c.r)[at]);
-                static_cast<T *>(c.out)[at] = from_f<T>(activate(v, c.act));
+                for (int i = 0; i < 4; ++i)
+                    e2m1_to_half(xa[i], xh[i]);
+                const float xscale = mx4_scale_value(xs[d]);
+#pragma unroll
+                for (int h = 0; h < kCh; ++h) {
+                    const uint32_t wa[4] = {wq[d][h].x, wq[d][h].y, wq[d][h].z, wq[d][h].w};
+                    __half2 sum[2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        __half2 wh[4];
+                        e2m1_to_half(wa[i], wh);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            sum[i / 2] = i % 2 == 0 && j == 0 ? __hmul2(wh[j], xh[i][j])
+                                                              : __hfma2(wh[j], xh[i][j], sum[i / 2]);
+                    }
+                    const float2 f = __half22float2(sum[0]), g = __half22float2(sum[1]);
+                    acc[h] = fmaf((f.x + f.y + (g.x + g.y)) * mx4_scale_value(ws[d][h]), xscale,
+                                  acc[h]);
+                }
             }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < kCh; ++h) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], d);
+        const int o = o0 + h;
+        if (lane == h && o < c.N) {
+            float v = acc[h] + (c.bias ? c.bias[o] : 0.f);
+            if (c.r)
+                v += to_f(static_cast<const T *>(c.r)[o]);
+            static_cast<T *>(c.out)[o] = from_f<T>(activate(v, c.act));
         }
     }
 }
@@ -182,6 +200,11 @@ int blocks_for(long long threads)
 template <typename T> const void *quantize_fn()
 {
     return reinterpret_cast<const void *>(quantize_kernel<T>);
+}
+template <typename T> const void *row_fn(int ch)
+{
+    return ch == 2 ? reinterpret_cast<const void *>(conv_row_kernel<T, 2>)
+                   : reinterpret_cast<const void *>(conv_row_kernel<T, 1>);
 }
 template <typename T> const void *dequantize_fn()
 {
@@ -213,19 +236,26 @@ int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtyp
                                                                               : X1CB_ERR_CUDA;
 }
 
+// One row: conv_row_kernel.  Up to 64: the weights as the MMA's rows, K split
+// over clusters (4096 x 4096: 16 rows 5.3 us, 64 rows 8.2 us, against 9.9 with
+// 128-row tiles; 128 rows 10.6 against 10.2).  More: 128-row tiles.
 int launch_conv_mx4(const Mx4Call &c, cudaStream_t s)
 {
-    if (c.M > 8)
+    if (c.M > 64)
         return launch_conv_mx4_tiles(c, s);
+    if (c.M > 1)
+        return launch_conv_mx4_split(c, s);
     Mx4Call a = c;
-    const void *k = c.dtype == X1CB_F32    ? reinterpret_cast<const void *>(conv_rows_kernel<float>)
-                    : c.dtype == X1CB_BF16 ? reinterpret_cast<const void *>(conv_rows_kernel<__nv_bfloat16>)
-                                           : reinterpret_cast<const void *>(conv_rows_kernel<__half>);
+    const int ch = c.N > 148 * 8 * 2 ? 2 : 1;
+    const void *k =
+        c.dtype == X1CB_F32    ? row_fn<float>(ch)
+        : c.dtype == X1CB_BF16 ? row_fn<__nv_bfloat16>(ch)
+                               : row_fn<__half>(ch);
     void *params[] = {&a};
-    const long long rows = (c.M + kRows - 1) / kRows;
-    const dim3 grid((c.N + kBlock / 32 - 1) / (kBlock / 32),
-                    static_cast<unsigned>(std::min<long long>(rows, 4096)));
-    return launch(k, grid, s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
+    const int per_block = kBlock / 32 * ch;
+    return launch(k, dim3((c.N + per_block - 1) / per_block), s, params) == cudaSuccess
+               ? X1CB_OK
+               : X1CB_ERR_CUDA;
 }
 
 }  // namespace x1cb
