@@ -488,11 +488,16 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_cuda_devices = {}
+
+
 def _empty(shape, dtype, index: int, stream):
     """A new tensor, allocated on the stream the call runs on, so that the
     allocator never hands out memory that work on another stream still uses, or
     takes back a workspace too early."""
-    device = torch.device("cuda", index)
+    device = _cuda_devices.get(index)
+    if device is None:
+        device = _cuda_devices.setdefault(index, torch.device("cuda", index))
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -503,13 +508,13 @@ def _empty(shape, dtype, index: int, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call(what: str, index: int, *args):
+def _call(fn, what: str, index: int, *args):
     """Runs the library call with GPU `index` current."""
-    if torch.cuda.current_device() == index:
-        status = getattr(lib(), what)(*args)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args)
     else:
         with torch.cuda.device(index):
-            status = getattr(lib(), what)(*args)
+            status = fn(*args)
     if status != X1CB_OK:
         raise X1cbError(status, what)
 
@@ -527,14 +532,18 @@ def _norm(what, x, gamma, beta, G, eps, r, act, outs, workspace, stream, q_mul=(
     shape = x.shape
     B, H, W, C = shape
     dt, a, index, G = _dtype(x.dtype, "x"), _act(act), _cuda_index(x, "x"), int(G)
-    _sized(gamma, (C,), "gamma")
-    _sized(beta, (C,), "beta")
-    _sized(r, shape, "r")
+    if gamma is not None:
+        _sized(gamma, (C,), "gamma")
+    if beta is not None:
+        _sized(beta, (C,), "beta")
+    if r is not None:
+        _sized(r, shape, "r")
     ys = outs(shape, index)
-    need = lib().group_norm_workspace_size(dt, B, H, W, C, G)
+    L = lib()
+    need = L.group_norm_workspace_size(dt, B, H, W, C, G)
     if workspace is None and need:
         workspace = _empty(need, torch.int8, index, stream)
-    _call(what, index, _ptr(x, x.dtype, index, "x"), dt, _ptr(gamma, torch.float32, index, "gamma"),
+    _call(getattr(L, what), what, index, _ptr(x, x.dtype, index, "x"), dt, _ptr(gamma, torch.float32, index, "gamma"),
           _ptr(beta, torch.float32, index, "beta"), _ptr(r, x.dtype, index, "r"), a, eps, *q_mul,
           *[_ptr(y, y.dtype, index, "out") for y in ys],
           _ptr(workspace, torch.int8, index, "workspace"),
@@ -618,7 +627,7 @@ def x1cb_quantize_mx4(x, out=None, stream=None):
     *lead, K = x.shape
     dt, index, M = _dtype(x.dtype, "x"), _cuda_index(x, "x"), x.numel() // K if K else 0
     q, sf = _mx4_outs(lead, M, K, out, index, stream)
-    _call("x1cb_quantize_mx4", index, _ptr(x, x.dtype, index, "x"), dt,
+    _call(lib().x1cb_quantize_mx4, "x1cb_quantize_mx4", index, _ptr(x, x.dtype, index, "x"), dt,
           _ptr(q, torch.uint8, index, "codes"), _ptr(sf, torch.uint8, index, "scales"), M, K,
           _raw_stream(stream, index))
     return q, sf
@@ -635,7 +644,7 @@ def x1cb_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None, stream=None):
     if out is None:
         out = _empty((*lead, K), dtype, index, stream)
     _sized(out, (*lead, K), "out")
-    _call("x1cb_dequantize_mx4", index, _ptr(q, torch.uint8, index, "codes"),
+    _call(lib().x1cb_dequantize_mx4, "x1cb_dequantize_mx4", index, _ptr(q, torch.uint8, index, "codes"),
           _ptr(sf, torch.uint8, index, "scales"), _ptr(out, dtype, index, "out"), dt, M, K,
           _raw_stream(stream, index))
     return out
@@ -666,7 +675,7 @@ def conv1x1_bias_add_act_mx4(x, xs, w, ws, bias=None, r=None, act: str = "relu",
         out = _empty(shape, dtype, index, stream)
     _sized(out, shape, "out")
     u8 = torch.uint8
-    _call("conv1x1_bias_add_act_mx4", index, _ptr(x, u8, index, "x"), _ptr(xs, u8, index, "xs"),
+    _call(lib().conv1x1_bias_add_act_mx4, "conv1x1_bias_add_act_mx4", index, _ptr(x, u8, index, "x"), _ptr(xs, u8, index, "xs"),
           _ptr(w, u8, index, "w"), _ptr(ws, u8, index, "ws"),
           _ptr(bias, torch.float32, index, "bias"), _ptr(r, dtype, index, "r"), a,
           _ptr(out, dtype, index, "out"), dt, B, H, W, Ic, Oc, _raw_stream(stream, index))

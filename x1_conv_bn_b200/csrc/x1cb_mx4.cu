@@ -14,85 +14,180 @@ namespace x1cb {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kDepth = 4;  // rows a thread has in flight
 
-// x -> MX4.  Each thread takes 16 bytes of x; the 32 / V neighbouring threads
-// of a block agree on its scale.  Every scale is a power of two, so scaling is
-// exact and the only rounding is the one to e2m1.
+// How a block of threads covers an [M, K] matrix in vectors: `rows` rows of nv
+// vectors at a time (or one row in pieces of kBlock vectors).
+struct Cover {
+    int M, K, nv, rows;
+};
+
+// Byte of a row's scales in the array, for the first block of the first tile.
+__device__ __forceinline__ size_t scale_row(uint32_t row, uint32_t kt)
+{
+    return static_cast<size_t>((row >> 7) * kt) * 512 + ((row & 31) * 16 + ((row >> 5) & 3) * 4);
+}
+
+// 16 bytes of x and the largest magnitude in them, as the bits of a float.
+template <typename T, int V> __device__ __forceinline__ uint32_t amax_bits(const Vec<T, V> &v)
+{
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            m = max(m, __float_as_uint(v.e[i]) & 0x7fffffffu);
+        return m;
+    } else {
+        // sign-free 16-bit patterns order as their values do, NaN above infinity
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+            m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        m = max(m >> 16, m & 0xffffu);
+        if constexpr (std::is_same<T, __half>::value)
+            return __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(m))));
+        else
+            return m << 16;
+    }
+}
+
+// x -> MX4.  Each thread takes 16 bytes of x, of kDepth rows at a time; the 32 / V
+// neighbouring threads of a block agree on its scale, and thread d of them stores
+// row d's.  Every scale is a power of two, so scaling is exact and the only
+// rounding is the one to e2m1.  Bound by memory and, close behind, by
+// instructions (the address arithmetic of one row at a time took half of them:
+// 59 us): KKK.
 template <typename T>
 __global__ void __launch_bounds__(kBlock)
     quantize_kernel(const T *__restrict__ x, uint8_t *__restrict__ q, uint8_t *__restrict__ sf,
-                    long long M, int K)
+                    const Cover c)
 {
     constexpr int V = 16 / sizeof(T), L = 32 / V;
+    static_assert(kDepth <= L, "a thread per row");
     griddep_wait();
-    const int kt = (K + 127) / 128, nv = K / V;
-    const long long n = M * nv;
+    const uint32_t kt = (c.K + 127) / 128;
     const int lane = threadIdx.x & 31;
     const uint32_t mask = ((1u << L) - 1u) << (lane & ~(L - 1));
-    const long long t0 = blockIdx.x * static_cast<long long>(kBlock) + threadIdx.x;
-    for (long long t = t0; t < n; t += static_cast<long long>(gridDim.x) * kBlock) {
-        const long long row = t / nv;
-        const int k = static_cast<int>(t - row * nv) * V;
-        const Vec<T, V> v = load_vec<T, V>(x + t * V);
-        float f[V];
-        uint32_t m = 0;
+    const int r0 = c.rows > 1 ? threadIdx.x / c.nv : 0;
+    if (r0 < c.rows) {
+        const int step = gridDim.x * c.rows;
+        const size_t x_step = static_cast<size_t>(step) * c.K;
+        for (int v = threadIdx.x - r0 * c.nv; v < c.nv; v += kBlock) {
+            const int blk = v / L;
+            const int pad = blk == c.K / 32 - 1 ? 3 - (blk & 3) : 0;
+            uint8_t *scales = sf + static_cast<size_t>(blk >> 2) * 512 + (blk & 3);
+            const int first = blockIdx.x * c.rows + r0;
+            const size_t at = static_cast<size_t>(first) * c.K + v * V;
+            const T *from = x + at;
+            uint8_t *to = q + at / 2;
+            // (rows count down, so that no row number overflows)
+            for (int left = c.M - first; left > 0;
+                 left = left > kDepth * step ? left - kDepth * step : 0) {
+                Vec<T, V> in[kDepth];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            f[i] = to_f(v.e[i]);
-            m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-        }
+                for (int d = 0; d < kDepth; ++d)
+                    if (left > d * step)
+                        in[d] = load_vec<T, V>(from + d * x_step);
+                from += kDepth * x_step;
+                uint32_t mine = 0;  // exponent bits of the row whose scale this thread stores
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1)
-            m = max(m, __shfl_xor_sync(mask, m, o));
-        const uint32_t s = mx4_scale_byte(m);
-        const float inv = mx4_inverse_scale(min(s, 252u));
+                for (int d = 0; d < kDepth; ++d) {
+                    if (left > d * step) {
+                        uint32_t m = amax_bits<T, V>(in[d]);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            f[i] *= inv;
-        if constexpr (V == 8)
-            reinterpret_cast<uint32_t *>(q)[t] = s == 255u ? 0u : e2m1x8(f);
-        else
-            reinterpret_cast<uint16_t *>(q)[t] = s == 255u ? uint16_t{0} : e2m1x4(f);
-        if ((lane & (L - 1)) == 0) {
-            const int blk = k / 32;
-            uint8_t *d = sf + mx4_scale_at(row, blk, kt);
-            *d = static_cast<uint8_t>(s);
-            if (blk == K / 32 - 1)
-                for (int j = 1; j < 4 - (blk & 3); ++j)
-                    d[j] = 0;
+                        for (int o = 1; o < L; o <<= 1)
+                            m = max(m, __shfl_xor_sync(mask, m, o));
+                        // exponent field e (at least 2): scale byte e - 2, inverse 2^(129 - e)
+                        const uint32_t e = max(m & 0x7f800000u, 0x01000000u);
+                        const float inv = __uint_as_float(0x80000000u - e);
+                        mine = (lane & (L - 1)) == d ? e : mine;
+                        F2 f[V / 2];
+                        unpack<T, V>(in[d], f);
+                        float y[V];
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            const float2 t = un2(mul2(f[i], f2(inv, inv)));
+                            y[2 * i] = t.x;
+                            y[2 * i + 1] = t.y;
+                        }
+                        const bool finite = e != 0x7f800000u;
+                        if constexpr (V == 8)
+                            *reinterpret_cast<uint32_t *>(to + d * (x_step / 2)) =
+                                finite ? e2m1x8(y) : 0u;
+                        else
+                            *reinterpret_cast<uint16_t *>(to + d * (x_step / 2)) =
+                                finite ? e2m1x4(y) : uint16_t{0};
+                    }
+                }
+                to += kDepth * (x_step / 2);
+                const int d = lane & (L - 1);
+                if (d < kDepth && left > d * step) {
+                    const uint32_t row = static_cast<uint32_t>(c.M - left) + d * step;
+                    uint8_t *d8 = scales + scale_row(row, kt);
+                    *d8 = static_cast<uint8_t>(mine == 0x7f800000u ? 255u : (mine >> 23) - 2u);
+                    for (int j = 1; j <= pad; ++j)
+                        d8[j] = 0;
+                }
+            }
         }
     }
     if (blockIdx.x == 0)
-        mx4_zero_row_padding(sf, M, kt, threadIdx.x, kBlock);
+        mx4_zero_row_padding(sf, c.M, kt, threadIdx.x, kBlock);
 }
 
-// MX4 -> values: eight codes a thread.
+// MX4 -> values: eight codes a thread, of kDepth rows at a time.  Bound by memory: KKK.
 template <typename T>
 __global__ void __launch_bounds__(kBlock)
     dequantize_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ sf,
-                      T *__restrict__ x, long long M, int K)
+                      T *__restrict__ x, const Cover c)
 {
     griddep_wait();
-    const int kt = (K + 127) / 128, nv = K / 8;
-    const long long n = M * nv;
-    for (long long t = blockIdx.x * static_cast<long long>(kBlock) + threadIdx.x; t < n;
-         t += static_cast<long long>(gridDim.x) * kBlock) {
-        const long long row = t / nv;
-        const int k = static_cast<int>(t - row * nv) * 8;
-        __half2 h[4];
-        e2m1_to_half(reinterpret_cast<const uint32_t *>(q)[t], h);
-        const float s = mx4_scale_value(sf[mx4_scale_at(row, k / 32, kt)]);
-        constexpr int V = 16 / sizeof(T);
+    const uint32_t kt = (c.K + 127) / 128;
+    const int r0 = c.rows > 1 ? threadIdx.x / c.nv : 0;
+    if (r0 >= c.rows)
+        return;
+    const int step = gridDim.x * c.rows;
+    const size_t x_step = static_cast<size_t>(step) * c.K;
+    for (int v = threadIdx.x - r0 * c.nv; v < c.nv; v += kBlock) {
+        const int blk = v / 4;
+        const uint8_t *scales = sf + static_cast<size_t>(blk >> 2) * 512 + (blk & 3);
+        const int first = blockIdx.x * c.rows + r0;
+        const size_t at = static_cast<size_t>(first) * c.K + v * 8;
+        const uint8_t *from = q + at / 2;
+        T *to = x + at;
+        for (int left = c.M - first; left > 0;
+             left = left > kDepth * step ? left - kDepth * step : 0) {
+            uint32_t codes[kDepth], s[kDepth];
+            const uint32_t row = static_cast<uint32_t>(c.M - left);
 #pragma unroll
-        for (int j = 0; j < 8; j += V) {
-            Vec<T, V> v;
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 f = __half22float2(h[(j + i) / 2]);
-                v.e[i] = from_f<T>(f.x * s);
-                v.e[i + 1] = from_f<T>(f.y * s);
+            for (int d = 0; d < kDepth; ++d) {
+                if (left > d * step) {
+                    codes[d] = __ldg(reinterpret_cast<const uint32_t *>(from + d * (x_step / 2)));
+                    s[d] = __ldg(scales + scale_row(row + d * step, kt));
+                }
             }
-            store_vec<T, V>(x + t * 8 + j, v);
+            from += kDepth * (x_step / 2);
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                if (left > d * step) {
+                    __half2 h[4];
+                    e2m1_to_half(codes[d], h);
+                    const float scale = mx4_scale_value(s[d]);
+                    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+                    for (int j = 0; j < 8; j += V) {
+                        F2 f[V / 2];
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            const float2 t = __half22float2(h[j / 2 + i]);
+                            f[i] = mul2(f2(t.x, t.y), f2(scale, scale));
+                        }
+                        store_vec<T, V>(to + d * x_step + j, finish<T, V>(f, X1CB_ACT_NONE));
+                    }
+                }
+            }
+            to += kDepth * x_step;
         }
     }
 }
@@ -192,9 +287,19 @@ cudaError_t launch(const void *kern, dim3 grid, cudaStream_t s, void **params)
     return cudaLaunchKernelExC(&cfg, kern, params);
 }
 
-int blocks_for(long long threads)
+Cover cover(long long M, int K, int nv)
 {
-    return static_cast<int>(std::min<long long>((threads + kBlock - 1) / kBlock, 148 * 32));
+    return Cover{static_cast<int>(M), K, nv, std::max(1, kBlock / nv)};
+}
+
+// Blocks for kDepth rows a thread, but no more than fill the chip eight deep.
+int blocks_for(const Cover &c)
+{
+    const long long per = static_cast<long long>(c.rows);
+    const long long all = (c.M + per - 1) / per;
+    const long long deep = (all + kDepth - 1) / kDepth;
+    return static_cast<int>(std::min<long long>(std::max<long long>(deep, std::min<long long>(all, 148)),
+                                                148 * 8));
 }
 
 template <typename T> const void *quantize_fn()
@@ -219,10 +324,9 @@ int launch_quantize_mx4(const void *x, int dtype, uint8_t *q, uint8_t *sf, long 
     const void *k = dtype == X1CB_F32    ? quantize_fn<float>()
                     : dtype == X1CB_BF16 ? quantize_fn<__nv_bfloat16>()
                                          : quantize_fn<__half>();
-    void *params[] = {&x, &q, &sf, &M, &K};
-    const int V = dtype == X1CB_F32 ? 4 : 8;
-    return launch(k, dim3(blocks_for(M * (K / V))), s, params) == cudaSuccess ? X1CB_OK
-                                                                              : X1CB_ERR_CUDA;
+    Cover c = cover(M, K, K / (dtype == X1CB_F32 ? 4 : 8));
+    void *params[] = {&x, &q, &sf, &c};
+    return launch(k, dim3(blocks_for(c)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
 }
 
 int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtype, long long M,
@@ -231,9 +335,9 @@ int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtyp
     const void *k = dtype == X1CB_F32    ? dequantize_fn<float>()
                     : dtype == X1CB_BF16 ? dequantize_fn<__nv_bfloat16>()
                                          : dequantize_fn<__half>();
-    void *params[] = {&q, &sf, &x, &M, &K};
-    return launch(k, dim3(blocks_for(M * (K / 8))), s, params) == cudaSuccess ? X1CB_OK
-                                                                              : X1CB_ERR_CUDA;
+    Cover c = cover(M, K, K / 8);
+    void *params[] = {&q, &sf, &x, &c};
+    return launch(k, dim3(blocks_for(c)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
 }
 
 // One row: conv_row_kernel.  Up to 64: the weights as the MMA's rows, K split
