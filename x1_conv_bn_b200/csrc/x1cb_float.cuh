@@ -151,6 +151,22 @@ template <int V> __device__ __forceinline__ void activate(float (&y)[V], int act
     }
 }
 
+// Largest magnitude, as the bits of a float; NaN if one is.
+template <int V> __device__ __forceinline__ uint32_t amax_bits(const float (&y)[V])
+{
+    static_assert(V == 4 || V == 8, "");
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(y[0])), "f"(fabsf(y[1])), "f"(fabsf(y[2])));
+    if constexpr (V == 4) {
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(y[3])));
+    } else {
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(y[3])), "f"(fabsf(y[4])));
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(y[5])), "f"(fabsf(y[6])));
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(y[7])));
+    }
+    return __float_as_uint(m);
+}
+
 // act(y) rounded to T, in one pass: ReLU is part of the 16-bit conversions.
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> finish(const F2 (&f)[kPairs<V>], int act)
@@ -222,20 +238,29 @@ __device__ __forceinline__ float mx4_scale_value(uint32_t s)
     return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
 }
 
-// Scale byte of a block whose largest magnitude has the float bits `amax`
-// (sign clear): the float's exponent field is floor(log2) + 127, so the byte
-// is that less 2 (the exponent of 4, the largest power of two in e2m1);
-// subnormals and zeros have field 0 and end at 0 with it.
-__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax)
+// A block's exponent bits from the bits of its largest magnitude: the float's
+// exponent field e, at least 2, where it stands in the float.  The scale byte is
+// e - 2 (e is floor(log2) + 127, and 4, the largest power of two in e2m1, takes
+// 2 of it; subnormals and zeros have field 0 and end at byte 0), the inverse
+// scale 2^(129 - e), exact; field 255 is a block with an infinity or NaN.
+constexpr uint32_t kMx4Bad = 0x7f800000u;
+__device__ __forceinline__ uint32_t mx4_exponent(uint32_t amax)
 {
-    const int e = static_cast<int>(amax >> 23);
-    return e == 255 ? 255u : static_cast<uint32_t>(max(e - 2, 0));
+    return max(amax & 0x7f800000u, 0x01000000u);
+}
+__device__ __forceinline__ float mx4_inverse_scale(uint32_t e)
+{
+    return __uint_as_float(0x80000000u - e);
+}
+__device__ __forceinline__ uint8_t mx4_scale_byte(uint32_t e)
+{
+    return static_cast<uint8_t>(e == kMx4Bad ? 255u : (e >> 23) - 2u);
 }
 
-// 2^(127 - s) for s <= 252 (a finite block's largest byte): exact.
-__device__ __forceinline__ float mx4_inverse_scale(uint32_t s)
+// Byte of a row's scales in the array, for the first block of the first tile.
+__device__ __forceinline__ size_t mx4_scale_row(uint32_t row, uint32_t kt)
 {
-    return __uint_as_float((254u - s) << 23);
+    return static_cast<size_t>((row >> 7) * kt) * 512 + ((row & 31) * 16 + ((row >> 5) & 3) * 4);
 }
 
 // Eight floats -> eight e2m1 codes (round to nearest even, saturating),

@@ -22,12 +22,6 @@ struct Cover {
     int M, K, nv, rows;
 };
 
-// Byte of a row's scales in the array, for the first block of the first tile.
-__device__ __forceinline__ size_t scale_row(uint32_t row, uint32_t kt)
-{
-    return static_cast<size_t>((row >> 7) * kt) * 512 + ((row & 31) * 16 + ((row >> 5) & 3) * 4);
-}
-
 // 16 bytes of x and the largest magnitude in them, as the bits of a float.
 template <typename T, int V> __device__ __forceinline__ uint32_t amax_bits(const Vec<T, V> &v)
 {
@@ -68,50 +62,53 @@ __global__ void __launch_bounds__(kBlock)
     griddep_wait();
     const uint32_t kt = (c.K + 127) / 128;
     const int lane = threadIdx.x & 31;
-    const uint32_t mask = ((1u << L) - 1u) << (lane & ~(L - 1));
+    // Whole warps go through the loops together, for the shuffles: a thread with
+    // nothing to do (behind the last row or vector) loads and stores nothing.
     const int r0 = c.rows > 1 ? threadIdx.x / c.nv : 0;
-    if (r0 < c.rows) {
-        const int step = gridDim.x * c.rows;
-        const size_t x_step = static_cast<size_t>(step) * c.K;
-        for (int v = threadIdx.x - r0 * c.nv; v < c.nv; v += kBlock) {
-            const int blk = v / L;
-            const int pad = blk == c.K / 32 - 1 ? 3 - (blk & 3) : 0;
-            uint8_t *scales = sf + static_cast<size_t>(blk >> 2) * 512 + (blk & 3);
-            const int first = blockIdx.x * c.rows + r0;
-            const size_t at = static_cast<size_t>(first) * c.K + v * V;
-            const T *from = x + at;
-            uint8_t *to = q + at / 2;
-            // (rows count down, so that no row number overflows)
-            for (int left = c.M - first; left > 0;
-                 left = left > kDepth * step ? left - kDepth * step : 0) {
-                Vec<T, V> in[kDepth];
+    const int step = gridDim.x * c.rows;
+    const size_t x_step = static_cast<size_t>(step) * c.K;
+    for (int v0 = 0; v0 < c.nv; v0 += kBlock) {
+        const int v = v0 + threadIdx.x - r0 * c.nv;
+        const bool active = r0 < c.rows && v < c.nv;
+        const int blk = v / L;
+        const int pad = blk == c.K / 32 - 1 ? 3 - (blk & 3) : 0;
+        uint8_t *scales = sf + static_cast<size_t>(blk >> 2) * 512 + (blk & 3);
+        const int first = blockIdx.x * c.rows + r0;
+        const size_t at = static_cast<size_t>(first) * c.K + v * V;
+        const T *from = x + at;
+        uint8_t *to = q + at / 2;
+        // (rows count down, so that no row number overflows)
+        int left = active ? c.M - first : 0;
+        for (int all = c.M - static_cast<int>(blockIdx.x) * c.rows; all > 0;
+             all = all > kDepth * step ? all - kDepth * step : 0) {
+            Vec<T, V> in[kDepth];
 #pragma unroll
-                for (int d = 0; d < kDepth; ++d)
-                    if (left > d * step)
-                        in[d] = load_vec<T, V>(from + d * x_step);
-                from += kDepth * x_step;
-                uint32_t mine = 0;  // exponent bits of the row whose scale this thread stores
+            for (int d = 0; d < kDepth; ++d)
+                if (left > d * step)
+                    in[d] = load_vec<T, V>(from + d * x_step);
+            from += kDepth * x_step;
+            uint32_t mine = 0;  // exponent bits of the row whose scale this thread stores
 #pragma unroll
-                for (int d = 0; d < kDepth; ++d) {
+            for (int d = 0; d < kDepth; ++d) {
+                if (all > d * step) {
+                    uint32_t m = amax_bits<T, V>(in[d]);
+#pragma unroll
+                    for (int o = 1; o < L; o <<= 1)
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const uint32_t e = mx4_exponent(m);
+                    const float inv = mx4_inverse_scale(e);
+                    mine = (lane & (L - 1)) == d ? e : mine;
+                    F2 f[V / 2];
+                    unpack<T, V>(in[d], f);
+                    float y[V];
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        const float2 t = un2(mul2(f[i], f2(inv, inv)));
+                        y[2 * i] = t.x;
+                        y[2 * i + 1] = t.y;
+                    }
                     if (left > d * step) {
-                        uint32_t m = amax_bits<T, V>(in[d]);
-#pragma unroll
-                        for (int o = 1; o < L; o <<= 1)
-                            m = max(m, __shfl_xor_sync(mask, m, o));
-                        // exponent field e (at least 2): scale byte e - 2, inverse 2^(129 - e)
-                        const uint32_t e = max(m & 0x7f800000u, 0x01000000u);
-                        const float inv = __uint_as_float(0x80000000u - e);
-                        mine = (lane & (L - 1)) == d ? e : mine;
-                        F2 f[V / 2];
-                        unpack<T, V>(in[d], f);
-                        float y[V];
-#pragma unroll
-                        for (int i = 0; i < V / 2; ++i) {
-                            const float2 t = un2(mul2(f[i], f2(inv, inv)));
-                            y[2 * i] = t.x;
-                            y[2 * i + 1] = t.y;
-                        }
-                        const bool finite = e != 0x7f800000u;
+                        const bool finite = e != kMx4Bad;
                         if constexpr (V == 8)
                             *reinterpret_cast<uint32_t *>(to + d * (x_step / 2)) =
                                 finite ? e2m1x8(y) : 0u;
@@ -120,16 +117,17 @@ __global__ void __launch_bounds__(kBlock)
                                 finite ? e2m1x4(y) : uint16_t{0};
                     }
                 }
-                to += kDepth * (x_step / 2);
-                const int d = lane & (L - 1);
-                if (d < kDepth && left > d * step) {
-                    const uint32_t row = static_cast<uint32_t>(c.M - left) + d * step;
-                    uint8_t *d8 = scales + scale_row(row, kt);
-                    *d8 = static_cast<uint8_t>(mine == 0x7f800000u ? 255u : (mine >> 23) - 2u);
-                    for (int j = 1; j <= pad; ++j)
-                        d8[j] = 0;
-                }
             }
+            to += kDepth * (x_step / 2);
+            const int d = lane & (L - 1);
+            if (d < kDepth && left > d * step) {
+                const uint32_t row = static_cast<uint32_t>(c.M - left) + d * step;
+                uint8_t *d8 = scales + mx4_scale_row(row, kt);
+                *d8 = mx4_scale_byte(mine);
+                for (int j = 1; j <= pad; ++j)
+                    d8[j] = 0;
+            }
+            left = left > kDepth * step ? left - kDepth * step : 0;
         }
     }
     if (blockIdx.x == 0)
@@ -164,7 +162,7 @@ __global__ void __launch_bounds__(kBlock)
             for (int d = 0; d < kDepth; ++d) {
                 if (left > d * step) {
                     codes[d] = __ldg(reinterpret_cast<const uint32_t *>(from + d * (x_step / 2)));
-                    s[d] = __ldg(scales + scale_row(row + d * step, kt));
+                    s[d] = __ldg(scales + mx4_scale_row(row + d * step, kt));
                 }
             }
             from += kDepth * (x_step / 2);
@@ -292,14 +290,14 @@ Cover cover(long long M, int K, int nv)
     return Cover{static_cast<int>(M), K, nv, std::max(1, kBlock / nv)};
 }
 
-// Blocks for kDepth rows a thread, but no more than fill the chip eight deep.
-int blocks_for(const Cover &c)
+// Blocks for kDepth rows a thread, but no more than `deep` per SM.  Writing more
+// than it reads, dequantisation gains from many short blocks (200704 x 512 to
+// bf16: 51.8 us with 8, 45.0 with 32); quantisation does not (45.3 and 49.3).
+int blocks_for(const Cover &c, int deep)
 {
-    const long long per = static_cast<long long>(c.rows);
-    const long long all = (c.M + per - 1) / per;
-    const long long deep = (all + kDepth - 1) / kDepth;
-    return static_cast<int>(std::min<long long>(std::max<long long>(deep, std::min<long long>(all, 148)),
-                                                148 * 8));
+    const int all = (c.M + c.rows - 1) / c.rows;
+    const int want = (all + kDepth - 1) / kDepth;
+    return std::min(std::max(want, std::min(all, 148)), 148 * deep);
 }
 
 template <typename T> const void *quantize_fn()
@@ -326,7 +324,7 @@ int launch_quantize_mx4(const void *x, int dtype, uint8_t *q, uint8_t *sf, long 
                                          : quantize_fn<__half>();
     Cover c = cover(M, K, K / (dtype == X1CB_F32 ? 4 : 8));
     void *params[] = {&x, &q, &sf, &c};
-    return launch(k, dim3(blocks_for(c)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
+    return launch(k, dim3(blocks_for(c, 8)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
 }
 
 int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtype, long long M,
@@ -337,7 +335,7 @@ int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtyp
                                          : dequantize_fn<__half>();
     Cover c = cover(M, K, K / 8);
     void *params[] = {&q, &sf, &x, &c};
-    return launch(k, dim3(blocks_for(c)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
+    return launch(k, dim3(blocks_for(c, 32)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
 }
 
 // One row: conv_row_kernel.  Up to 64: the weights as the MMA's rows, K split

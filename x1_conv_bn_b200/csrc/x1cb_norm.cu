@@ -318,7 +318,10 @@ template <typename T, int V, int OUT> struct Out {
             pad = blk == a.C / 32 - 1 ? 3 - (blk & 3) : 0;
         }
     }
-    __device__ __forceinline__ void put(const NormArgs &a, const F2 (&f)[kPairs<V>])
+    // MX4: whole warps call it, `valid` says whether this thread has a pixel (a
+    // block's threads share one); the others call it with a pixel only.
+    static constexpr bool kWhole = OUT == kNormMx4;
+    __device__ __forceinline__ void put(const NormArgs &a, const F2 (&f)[kPairs<V>], bool valid)
     {
         if constexpr (OUT == kNormSame) {
             store_vec<T, V>(reinterpret_cast<T *>(to), finish<T, V>(f, a.act));
@@ -353,33 +356,34 @@ template <typename T, int V, int OUT> struct Out {
                 else
                     *reinterpret_cast<uint32_t *>(to) = w[0];
             } else {
-                // The 32 / V neighbouring threads that hold a block agree on its
-                // scale (they belong to one pixel, so they are here together).
+                // The 32 / V neighbouring threads that hold a block agree on its scale.
+                // (With a mask of its own for each block, the shuffles of a warp run
+                // one after the other: 57 us for 128 x 28 x 28 x 512, KKK with whole
+                // warps.)
                 constexpr int L = 32 / V;
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-                const int lane = threadIdx.x & 31;
-                const uint32_t mask = ((1u << L) - 1u) << (lane & ~(L - 1));
+                uint32_t m = amax_bits(y);
 #pragma unroll
                 for (int o = 1; o < L; o <<= 1)
-                    m = max(m, __shfl_xor_sync(mask, m, o));
-                const uint32_t s = mx4_scale_byte(m);
-                const float inv = mx4_inverse_scale(min(s, 252u));
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const uint32_t e = mx4_exponent(m);
+                const float inv = mx4_inverse_scale(e);
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    y[i] *= inv;
-                if constexpr (V == 8)
-                    *reinterpret_cast<uint32_t *>(to) = s == 255u ? 0u : e2m1x8(y);
-                else
-                    *reinterpret_cast<uint16_t *>(to) = s == 255u ? uint16_t{0} : e2m1x4(y);
-                if ((lane & (L - 1)) == 0) {
-                    uint8_t *d = scales + static_cast<size_t>(row >> 7) * kt * 512 +
-                                 (row & 31) * 16 + ((row >> 5) & 3) * 4;
-                    *d = static_cast<uint8_t>(s);
-                    for (int k = 1; k <= pad; ++k)
-                        d[k] = 0;
+                for (int i = 0; i < V; i += 2) {
+                    const float2 t = un2(mul2(f2(y[i], y[i + 1]), f2(inv, inv)));
+                    y[i] = t.x;
+                    y[i + 1] = t.y;
+                }
+                if (valid) {
+                    if constexpr (V == 8)
+                        *reinterpret_cast<uint32_t *>(to) = e == kMx4Bad ? 0u : e2m1x8(y);
+                    else
+                        *reinterpret_cast<uint16_t *>(to) = e == kMx4Bad ? uint16_t{0} : e2m1x4(y);
+                    if ((threadIdx.x & (L - 1)) == 0) {
+                        uint8_t *d = scales + mx4_scale_row(row, kt);
+                        *d = mx4_scale_byte(e);
+                        for (int k = 1; k <= pad; ++k)
+                            d[k] = 0;
+                    }
                 }
                 row += a.lanes;
             }
@@ -439,18 +443,27 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
     const int pl = quotient(threadIdx.x, a.div_nv);
     const int per_lane = quotient(px, a.div_lanes), more = px - per_lane * a.lanes;
     const int mine = pl < a.lanes ? per_lane + (pl < more) : 0;
+    using O = Out<T, V, OUT>;
+    const int most = O::kWhole ? per_lane + (more > 0) : mine;  // of the block
     const size_t step = static_cast<size_t>(a.lanes) * a.C;
-    for (int cv = threadIdx.x - pl * a.nv; cv < a.nv && mine > 0; cv += kBlock) {
-        const Affine<T, V> f(a, coef, cv * V, cv * V, a.cg % V == 0);
-        const size_t base = (static_cast<size_t>(b) * a.HW + p0 + pl) * a.C + cv * V;
+    // (C is a multiple of 32 for MX4, and with it the threads of a pixel: a warp's
+    // threads leave this loop together but for those without a pixel)
+    for (int cv0 = 0; cv0 < a.nv; cv0 += kBlock) {
+        const int cv = cv0 + threadIdx.x - pl * a.nv;
+        const bool active = mine > 0 && cv < a.nv;
+        if (!O::kWhole && !active)
+            continue;
+        const int c = active ? cv * V : 0, n = active ? mine : 0;
+        const Affine<T, V> f(a, coef, c, c, a.cg % V == 0);
+        const size_t base = (static_cast<size_t>(b) * a.HW + p0 + (active ? pl : 0)) * a.C + c;
         const T *x = static_cast<const T *>(a.x) + base;
         const T *r = a.r ? static_cast<const T *>(a.r) + base : nullptr;
-        Out<T, V, OUT> out(a, b, p0 + pl, cv * V);
-        for (int i0 = 0; i0 < mine; i0 += kBatch) {
+        O out(a, b, p0 + (active ? pl : 0), c);
+        for (int i0 = 0; i0 < most; i0 += kBatch) {
             Vec<T, V> v[kBatch], rv[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                if (i0 + j < mine) {
+                if (i0 + j < n) {
                     v[j] = load_vec<T, V>(x + j * step);
                     if (r)
                         rv[j] = load_vec<T, V>(r + j * step);
@@ -461,10 +474,10 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
                 r += kBatch * step;
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                if (i0 + j < mine) {
+                if (O::kWhole ? i0 + j < most : i0 + j < n) {
                     F2 y[kPairs<V>];
                     f.apply(v[j], r ? &rv[j] : nullptr, y);
-                    out.put(a, y);
+                    out.put(a, y, i0 + j < n);
                 }
             }
         }
@@ -588,19 +601,23 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
     }
     copy_wait<0>();
     __syncthreads();
-    if (mine > 0) {
-        const Affine<T, V> f(a, coef, c, cv * V, one);
-        Out<T, V, OUT> out(a, b, p0 + pl, c);
+    using O = Out<T, V, OUT>;
+    const int most = O::kWhole ? per_lane + (more > 0) : mine;  // pixels of the CTA's first lane
+    if (most > 0) {
+        const bool active = mine > 0;  // (threads without a pixel: any channel of the slice)
+        const int cs = active ? cv * V : 0, c1 = active ? c : c - cv * V;
+        const Affine<T, V> f(a, coef, c1, cs, one);
+        O out(a, b, p0 + (active ? pl : 0), c1);
         if (a.stage_r || !r) {
             const int second = r ? a.iters * kBlock : 0;
 #pragma unroll 2
-            for (int i = 0; i < mine; ++i) {
+            for (int i = 0; i < most; ++i) {
                 F2 y[kPairs<V>];
                 f.apply(slots[i * kBlock], r ? &slots[second + i * kBlock] : nullptr, y);
-                out.put(a, y);
+                out.put(a, y, i < mine);
             }
         } else {
-            for (int i0 = 0; i0 < mine; i0 += kBatch, r += kBatch * step) {
+            for (int i0 = 0; i0 < most; i0 += kBatch, r += kBatch * step) {
                 Slot rv[kBatch];
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j)
@@ -608,10 +625,10 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
                         rv[j] = load_vec<T, V>(r + j * step);
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
-                    if (i0 + j < mine) {
+                    if (i0 + j < most) {
                         F2 y[kPairs<V>];
                         f.apply(slots[(i0 + j) * kBlock], &rv[j], y);
-                        out.put(a, y);
+                        out.put(a, y, i0 + j < mine);
                     }
                 }
             }
