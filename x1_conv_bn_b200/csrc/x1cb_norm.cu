@@ -193,14 +193,29 @@ __device__ __forceinline__ Coef make_coef(const Joined &j, double inv_count, flo
     return c;
 }
 
+// gamma and beta of V channels from c on, loaded ahead of the statistics.
+template <int V> struct Params {
+    float gamma[V], beta[V];
+    __device__ __forceinline__ Params(const NormArgs &a, int c)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            gamma[i] = a.gamma ? __ldg(a.gamma + c + i) : 1.f;
+            beta[i] = a.beta ? __ldg(a.beta + c + i) : 0.f;
+        }
+    }
+};
+
 // The normalisation of V channels.  16-bit inputs: y = x * sc + be, be = beta -
 // mu * sc; what rounding be loses is far below the input's own step.  32-bit
 // inputs: y = (x - mu) * sc + be with the mean's low part in be.
 template <typename T, int V> struct Affine {
     static constexpr bool kSub = sizeof(T) == 4;
     F2 mu[kSub ? kPairs<V> : 1], sc[kPairs<V>], be[kPairs<V>];
-    // c: the first channel, cs: the same counted from the slice's first group
-    __device__ __forceinline__ Affine(const NormArgs &a, const Coef *coef, int c, int cs, bool one)
+    // p: gamma and beta of the channels; cs: the first of them, counted from the
+    // slice's first group
+    __device__ __forceinline__ Affine(const NormArgs &a, const Coef *coef, const Params<V> &p, int cs,
+                                      bool one)
     {
         float m[V + 1], s[V + 1], b[V + 1];
         m[V] = s[V] = b[V] = 0.f;
@@ -212,8 +227,8 @@ template <typename T, int V> struct Affine {
                 k = coef[++g];
                 left = a.cg;
             }
-            s[i] = a.gamma ? k.rstd * a.gamma[c + i] : k.rstd;
-            const float beta = a.beta ? a.beta[c + i] : 0.f;
+            s[i] = k.rstd * p.gamma[i];
+            const float beta = p.beta[i];
             m[i] = -k.mu;
             b[i] = fmaf(-k.mu_low, s[i], kSub ? beta : fmaf(-k.mu, s[i], beta));
         }
@@ -259,18 +274,19 @@ template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stat
         for (int cv = threadIdx.x - pl * a.nv; cv < a.nv && mine > 0; cv += kBlock) {
             const T *x = static_cast<const T *>(a.x) +
                          (static_cast<size_t>(b) * a.HW + p0 + pl) * a.C + cv * V;
+            constexpr int kDeep = 2 * kBatch;
             Sums<V> st;
-            Vec<T, V> v[kBatch];
-            for (int i0 = 0; i0 < mine; i0 += kBatch) {
+            Vec<T, V> v[kDeep];
+            for (int i0 = 0; i0 < mine; i0 += kDeep) {
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j)
+                for (int j = 0; j < kDeep; ++j)
                     if (i0 + j < mine)
                         v[j] = load_vec<T, V>(x + j * step);
-                x += kBatch * step;
+                x += kDeep * step;
                 if (i0 == 0)
                     st.start(v[0]);
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j)
+                for (int j = 0; j < kDeep; ++j)
                     if (i0 + j < mine)
                         st.add(v[j]);
             }
@@ -316,6 +332,66 @@ template <typename T, int V, int OUT> struct Out {
             scales = a.sf + static_cast<size_t>(blk >> 2) * 512 + (blk & 3);
             row = static_cast<uint32_t>(at);
             pad = blk == a.C / 32 - 1 ? 3 - (blk & 3) : 0;
+        }
+    }
+    // MX4, the next kBatch pixels (n of them the thread's) at once, so that their
+    // shuffles are in flight together: thread j of a block's threads stores the
+    // scale of pixel j.  Whole warps call it.
+    template <typename Value>
+    __device__ __forceinline__ void put_batch(const NormArgs &a, int n, const Value &value)
+    {
+        if constexpr (OUT == kNormMx4) {
+            constexpr int L = 32 / V;
+            static_assert(kBatch <= L, "a thread per pixel");
+            float y[kBatch][V];
+            uint32_t m[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                F2 f[kPairs<V>];
+                value(j, f);
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const float2 t = un2(f[i]);
+                    y[j][2 * i] = t.x;
+                    y[j][2 * i + 1] = t.y;
+                }
+                activate(y[j], a.act);
+                m[j] = amax_bits(y[j]);
+            }
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
+            const int lane = threadIdx.x & (L - 1);
+            uint32_t mine = 0;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const uint32_t e = mx4_exponent(m[j]);
+                const float inv = mx4_inverse_scale(e);
+                mine = lane == j ? e : mine;
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 t = un2(mul2(f2(y[j][i], y[j][i + 1]), f2(inv, inv)));
+                    y[j][i] = t.x;
+                    y[j][i + 1] = t.y;
+                }
+                if (j < n) {
+                    if constexpr (V == 8)
+                        *reinterpret_cast<uint32_t *>(to) = e == kMx4Bad ? 0u : e2m1x8(y[j]);
+                    else
+                        *reinterpret_cast<uint16_t *>(to) =
+                            e == kMx4Bad ? uint16_t{0} : e2m1x4(y[j]);
+                }
+                to += step;
+            }
+            if (lane < min(n, kBatch)) {
+                uint8_t *d = scales + mx4_scale_row(row + lane * a.lanes, kt);
+                *d = mx4_scale_byte(mine);
+                for (int k = 1; k <= pad; ++k)
+                    d[k] = 0;
+            }
+            row += kBatch * a.lanes;
         }
     }
     // MX4: whole warps call it, `valid` says whether this thread has a pixel (a
@@ -454,7 +530,7 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
         if (!O::kWhole && !active)
             continue;
         const int c = active ? cv * V : 0, n = active ? mine : 0;
-        const Affine<T, V> f(a, coef, c, c, a.cg % V == 0);
+        const Affine<T, V> f(a, coef, Params<V>(a, c), c, a.cg % V == 0);
         const size_t base = (static_cast<size_t>(b) * a.HW + p0 + (active ? pl : 0)) * a.C + c;
         const T *x = static_cast<const T *>(a.x) + base;
         const T *r = a.r ? static_cast<const T *>(a.r) + base : nullptr;
@@ -564,6 +640,9 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
             st.write(mine, one, buf + threadIdx.x * per);
         }
     }
+    const bool active = mine > 0;  // (threads without a pixel: any channel of the slice)
+    const int cs = active ? cv * V : 0, c1 = active ? c : c - cv * V;
+    const Params<V> params(a, c1);
     __syncthreads();
     {
         const int w = join_width(groups), width = a.cg / each, pitch = a.Cs / each;
@@ -604,11 +683,17 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
     using O = Out<T, V, OUT>;
     const int most = O::kWhole ? per_lane + (more > 0) : mine;  // pixels of the CTA's first lane
     if (most > 0) {
-        const bool active = mine > 0;  // (threads without a pixel: any channel of the slice)
-        const int cs = active ? cv * V : 0, c1 = active ? c : c - cv * V;
-        const Affine<T, V> f(a, coef, c1, cs, one);
+        const Affine<T, V> f(a, coef, params, cs, one);
         O out(a, b, p0 + (active ? pl : 0), c1);
-        if (a.stage_r || !r) {
+        if (O::kWhole && (a.stage_r || !r)) {
+            // (slots past a thread's pixels hold nothing, and nothing of them is stored)
+            const int second = r ? a.iters * kBlock : 0;
+            for (int i0 = 0; i0 < most; i0 += kBatch)
+                out.put_batch(a, mine - i0, [&](int j, F2(&y)[kPairs<V>]) {
+                    const int i = min(i0 + j, a.iters - 1) * kBlock;
+                    f.apply(slots[i], r ? &slots[second + i] : nullptr, y);
+                });
+        } else if (a.stage_r || !r) {
             const int second = r ? a.iters * kBlock : 0;
 #pragma unroll 2
             for (int i = 0; i < most; ++i) {
@@ -653,7 +738,7 @@ int vector_channels(int dtype, int n)
 // What either form needs to know of a call.
 struct Plan {
     int V, nv, lanes;
-    int chunks, chunk;                    // two-launch form
+    int chunks, chunk, images;            // two-launch form: per image; images at a time
     int cluster, Cs, slices, iters, smem;  // cluster form (cluster = 0: two launches)
     int stage_r;
 };
@@ -731,8 +816,12 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool r
         return p;
     p.nv = C / p.V;
     p.lanes = std::max(1, kBlock / p.nv);
-    // three blocks per SM at once, at least two batches a thread
-    const long long want = std::max(1, 148 * 3 / B);
+    // As many images at a time as L2 (126 MB) holds beside what is written, in
+    // equal turns; three blocks per SM, at least two batches a thread.
+    const double image = static_cast<double>(HW) * C * elt;
+    const int turns = static_cast<int>(std::min<double>(B, std::ceil(B * image / 60e6)));
+    p.images = std::min((B + turns - 1) / turns, 65535);
+    const long long want = std::max(1, 148 * 3 / p.images);
     const long long most = std::max(1, HW / (p.lanes * kBatch * 2));
     p.chunks = static_cast<int>(std::min(want, most));
     p.chunk = std::min((HW + p.chunks - 1) / p.chunks, kFold * p.lanes);
@@ -796,11 +885,8 @@ int run(const NormCall &c, const Plan &p, NormArgs a, cudaStream_t s)
         return e;
     if (int e = opt_apply(ka))
         return e;
-    // as many images at a time as L2 (126 MB) holds beside what is written
-    const double image = static_cast<double>(c.HW) * c.C * sizeof(T);
-    const int most = static_cast<int>(std::min(65535., std::max(1., 40e6 / image)));
-    for (a.b0 = 0; a.b0 < c.B; a.b0 += most) {
-        const dim3 grid(p.chunks, std::min(most, c.B - a.b0));
+    for (a.b0 = 0; a.b0 < c.B; a.b0 += p.images) {
+        const dim3 grid(p.chunks, std::min(p.images, c.B - a.b0));
         if (int e = launch(ks, grid, static_cast<size_t>(p.lanes) * c.C * sizeof(float2), 1, s, a))
             return e;
         if (int e = launch(ka, grid, static_cast<size_t>(c.G) * sizeof(Coef), 1, s, a))
