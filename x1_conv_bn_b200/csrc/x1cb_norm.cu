@@ -307,7 +307,7 @@ template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stat
 
 // Where a thread's outputs go: channels c .. c + V - 1 of pixel p of image b,
 // and of every `lanes`-th pixel after it.
-template <typename T, int V, int OUT> struct Out {
+template <typename T, int V, int OUT, bool kStream = false> struct Out {
     uint8_t *to;       // the next output, code or int8
     size_t step;       // bytes to the one after it
     uint8_t *scales;   // MX4: the scale array from this block of channels on
@@ -400,7 +400,11 @@ template <typename T, int V, int OUT> struct Out {
     __device__ __forceinline__ void put(const NormArgs &a, const F2 (&f)[kPairs<V>], bool valid)
     {
         if constexpr (OUT == kNormSame) {
-            store_vec<T, V>(reinterpret_cast<T *>(to), finish<T, V>(f, a.act));
+            const Vec<T, V> v = finish<T, V>(f, a.act);
+            if constexpr (kStream && sizeof(v) == 16)
+                __stcs(reinterpret_cast<uint4 *>(to), *reinterpret_cast<const uint4 *>(&v));
+            else
+                store_vec<T, V>(reinterpret_cast<T *>(to), v);
         } else {
             float y[V];
 #pragma unroll
@@ -473,8 +477,9 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
 {
     extern __shared__ Coef coef[];  // [G]
     griddep_wait();
-    const int b = a.b0 + blockIdx.y;
-    const int p0 = blockIdx.x * a.chunk, px = min(a.HW - p0, a.chunk);
+    // The last chunks first: they are the ones that the statistics left in L2.
+    const int b = a.b0 + gridDim.y - 1 - blockIdx.y;
+    const int p0 = (gridDim.x - 1 - blockIdx.x) * a.chunk, px = min(a.HW - p0, a.chunk);
     // Join the chunks' statistics, in 64 bits.
     const int w = join_width(a.G);
     const double last = static_cast<double>(a.HW - (a.chunks - 1) * a.chunk) * a.cg;
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
     const int pl = quotient(threadIdx.x, a.div_nv);
     const int per_lane = quotient(px, a.div_lanes), more = px - per_lane * a.lanes;
     const int mine = pl < a.lanes ? per_lane + (pl < more) : 0;
-    using O = Out<T, V, OUT>;
+    using O = Out<T, V, OUT, true>;  // (results do not push the input out of L2)
     const int most = O::kWhole ? per_lane + (more > 0) : mine;  // of the block
     const size_t step = static_cast<size_t>(a.lanes) * a.C;
     // (C is a multiple of 32 for MX4, and with it the threads of a pixel: a warp's
@@ -774,7 +779,10 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool r
     long long unit = cg;
     while (unit % p.V || (whole_blocks && unit % 32))
         unit += cg;
-    double best = 1e30;
+    // The two launches, in us: 28.9 MB of input 22.9, 51.4 MB 33.0, 205 MB 123.  The
+    // form is chosen without regard to a shortcut, for the workspace's sake.
+    const double two = 10. + 0.55e-6 * B * static_cast<double>(HW) * C * elt;
+    double best = 1e30, plain = 1e30;
     for (int n = 1; n * unit <= C; ++n) {
         if (C % (n * unit))
             continue;
@@ -799,6 +807,7 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool r
             if (ctas > INT_MAX)
                 continue;
             const double cost = norm_cost(ctas, smem, Cs * elt, k, res && !stage_r);
+            plain = std::min(plain, res ? norm_cost(ctas, rest + data, Cs * elt, k, false) : cost);
             if (cost < best) {
                 best = cost;
                 p.cluster = k;
@@ -812,16 +821,18 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool r
             }
         }
     }
-    if (p.cluster)
+    if (p.cluster && plain <= two)
         return p;
+    p.cluster = 0;
     p.nv = C / p.V;
     p.lanes = std::max(1, kBlock / p.nv);
     // As many images at a time as L2 (126 MB) holds beside what is written, in
-    // equal turns; three blocks per SM, at least two batches a thread.
+    // equal turns; two blocks per SM (each joins all of its image's chunks: 512 x 512 x
+    // 128 51 us with two, 62 with three, 117 with six), at least two batches a thread.
     const double image = static_cast<double>(HW) * C * elt;
     const int turns = static_cast<int>(std::min<double>(B, std::ceil(B * image / 60e6)));
     p.images = std::min((B + turns - 1) / turns, 65535);
-    const long long want = std::max(1, 148 * 3 / p.images);
+    const long long want = std::max(1, 148 * 2 / p.images);
     const long long most = std::max(1, HW / (p.lanes * kBatch * 2));
     p.chunks = static_cast<int>(std::min(want, most));
     p.chunk = std::min((HW + p.chunks - 1) / p.chunks, kFold * p.lanes);
