@@ -524,32 +524,33 @@ def group_norm_workspace_size(dtype, B: int, H: int, W: int, C: int, G: int) -> 
     return int(lib().group_norm_workspace_size(_dtype(dtype, "dtype"), B, H, W, C, G))
 
 
-def _norm(what, x, gamma, beta, G, eps, r, act, outs, workspace, stream, q_mul=()):
-    """Shared by the group_norm_act calls; outs(shape, index) allocates or
-    checks the outputs."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 4:
-        raise ValueError("x must be [B, H, W, C]")
-    shape = x.shape
+def _norm(fn, what, x, gamma, beta, G, eps, r, act, ys, index, workspace, stream, *q_mul):
+    """Shared by the group_norm_act calls, behind the checks of their outputs."""
+    shape, xt = x.shape, x.dtype
     B, H, W, C = shape
-    dt, a, index, G = _dtype(x.dtype, "x"), _act(act), _cuda_index(x, "x"), int(G)
-    if gamma is not None:
+    dt = DTYPES[xt]
+    if gamma is not None and gamma.shape != (C,):
         _sized(gamma, (C,), "gamma")
-    if beta is not None:
+    if beta is not None and beta.shape != (C,):
         _sized(beta, (C,), "beta")
-    if r is not None:
+    if r is not None and r.shape != shape:
         _sized(r, shape, "r")
-    ys = outs(shape, index)
-    L = lib()
-    need = L.group_norm_workspace_size(dt, B, H, W, C, G)
+    need = lib().group_norm_workspace_size(dt, B, H, W, C, G)
     if workspace is None and need:
         workspace = _empty(need, torch.int8, index, stream)
-    _call(getattr(L, what), what, index, _ptr(x, x.dtype, index, "x"), dt, _ptr(gamma, torch.float32, index, "gamma"),
-          _ptr(beta, torch.float32, index, "beta"), _ptr(r, x.dtype, index, "r"), a, eps, *q_mul,
-          *[_ptr(y, y.dtype, index, "out") for y in ys],
-          _ptr(workspace, torch.int8, index, "workspace"),
+    _call(fn, what, index, _ptr(x, xt, index, "x"), dt, _ptr(gamma, torch.float32, index, "gamma"),
+          _ptr(beta, torch.float32, index, "beta"), _ptr(r, xt, index, "r"), _act(act), eps, *q_mul,
+          *ys, _ptr(workspace, torch.int8, index, "workspace"),
           0 if workspace is None else workspace.numel(), B, H, W, C, G,
           _raw_stream(stream, index))
-    return ys
+
+
+def _norm_input(x):
+    """(index of x's GPU, shape) of a group norm's input."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError("x must be [B, H, W, C]")
+    _dtype(x.dtype, "x")
+    return _cuda_index(x, "x"), x.shape
 
 
 def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str = "relu",
@@ -558,31 +559,29 @@ def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str =
 
     x, r, out [B, H, W, C] float32, bfloat16 or float16; gamma, beta [C]
     float32 or None; G groups; act "none", "relu" or "silu"."""
-    def outs(shape, index):
-        if out is None:
-            return (_empty(shape, x.dtype, index, stream),)
-        if out.dtype != x.dtype:
-            raise ValueError(f"out must be {x.dtype}, got {out.dtype}")
-        return (_sized(out, shape, "out"),)
-
-    return _norm("group_norm_act", x, gamma, beta, G, eps, r, act, outs, workspace, stream)[0]
+    index, shape = _norm_input(x)
+    if out is None:
+        out = _empty(shape, x.dtype, index, stream)
+    elif out.shape != shape:
+        _sized(out, shape, "out")
+    _norm(lib().group_norm_act, "group_norm_act", x, gamma, beta, int(G), eps, r, act,
+          (_ptr(out, x.dtype, index, "out"),), index, workspace, stream)
+    return out
 
 
 def group_norm_act_i8(x, gamma, beta, G: int, q_mul: float, eps: float = 1e-5, r=None,
                       act: str = "relu", out=None, workspace=None, stream=None):
     """group_norm_act quantised for the int8 convolutions: clamp(rint(y * q_mul),
     -128, 127) as NC/32HW32 [B, C/32, H, W, 32]."""
-    def outs(shape, index):
-        B, H, W, C = shape
-        shape = (B, C // 32, H, W, 32)
-        if out is None:
-            return (_empty(shape, torch.int8, index, stream),)
-        if out.dtype != torch.int8:
-            raise ValueError(f"out must be int8, got {out.dtype}")
-        return (_sized(out, shape, "out"),)
-
-    return _norm("group_norm_act_i8", x, gamma, beta, G, eps, r, act, outs, workspace, stream,
-                 (float(q_mul),))[0]
+    index, (B, H, W, C) = _norm_input(x)
+    shape = (B, C // 32, H, W, 32)
+    if out is None:
+        out = _empty(shape, torch.int8, index, stream)
+    else:
+        _sized(out, shape, "out")
+    _norm(lib().group_norm_act_i8, "group_norm_act_i8", x, gamma, beta, int(G), eps, r, act,
+          (_ptr(out, torch.int8, index, "out"),), index, workspace, stream, q_mul)
+    return out
 
 
 def mx4_scale_shape(M: int, K: int):
@@ -597,9 +596,6 @@ def _mx4_outs(lead, M, K, out, index, stream):
         return (_empty(shape, torch.uint8, index, stream),
                 _empty(scales, torch.uint8, index, stream))
     q, sf = out
-    for t, name in ((q, "codes"), (sf, "scales")):
-        if t.dtype != torch.uint8:
-            raise ValueError(f"{name} must be uint8, got {t.dtype}")
     return (_sized(q, shape, "codes"), _sized(sf, scales, "scales"))
 
 
@@ -607,11 +603,12 @@ def group_norm_act_mx4(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: s
                        out=None, workspace=None, stream=None):
     """group_norm_act quantised to MX4: (codes [B, H, W, C/2], scales), the
     operand of conv1x1_bias_add_act_mx4."""
-    def outs(shape, index):
-        B, H, W, C = shape
-        return _mx4_outs((B, H, W), B * H * W, C, out, index, stream)
-
-    return _norm("group_norm_act_mx4", x, gamma, beta, G, eps, r, act, outs, workspace, stream)
+    index, (B, H, W, C) = _norm_input(x)
+    q, sf = _mx4_outs((B, H, W), B * H * W, C, out, index, stream)
+    _norm(lib().group_norm_act_mx4, "group_norm_act_mx4", x, gamma, beta, int(G), eps, r, act,
+          (_ptr(q, torch.uint8, index, "codes"), _ptr(sf, torch.uint8, index, "scales")), index,
+          workspace, stream)
+    return q, sf
 
 
 def x1cb_mx4_scale_size(M: int, K: int) -> int:

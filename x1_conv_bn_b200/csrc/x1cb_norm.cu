@@ -769,7 +769,7 @@ double norm_cost(double ctas, double smem, int segment, int cluster, bool direct
     return t * (fit == 1 ? 1.2 : 1.);
 }
 
-Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool res)
+Plan search_plan(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool res)
 {
     Plan p{};
     const int elt = dtype == X1CB_F32 ? 4 : 2, cg = C / G;
@@ -838,6 +838,29 @@ Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool r
     p.chunk = std::min((HW + p.chunks - 1) / p.chunks, kFold * p.lanes);
     p.chunks = (HW + p.chunk - 1) / p.chunk;
     return p;
+}
+
+// The search takes about a microsecond, as long as the launch of a small call
+// takes on the host: each thread keeps the last plans (by shape).
+Plan plan_norm(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool res)
+{
+    struct Entry {
+        int key[7];
+        Plan plan;
+    };
+    constexpr int kKept = 8;
+    static thread_local Entry kept[kKept];
+    static thread_local int used = 0, next = 0;
+    const int key[7] = {dtype, B, HW, C, G, whole_blocks, res};
+    for (int i = 0; i < used; ++i)
+        if (std::memcmp(kept[i].key, key, sizeof(key)) == 0)
+            return kept[i].plan;
+    Entry &e = kept[next];
+    std::memcpy(e.key, key, sizeof(key));
+    e.plan = search_plan(dtype, B, HW, C, G, whole_blocks, res);
+    next = (next + 1) % kKept;
+    used = std::min(used + 1, kKept);
+    return e.plan;
 }
 
 // Sets a kernel's shared-memory limit once per device.
