@@ -438,6 +438,23 @@ def x1cb_pack_weight(oihw, out=None, stream=None):
 
 # ---- floating-point operators ------------------------------------------------
 
+# Calls in their ordinary form (operands on the current device, results new, on
+# the current stream) are marshalled by the compiled module _x1cb_torch, which
+# answers None to anything else; the Python below takes that, and names what is
+# wrong.
+_fast = None
+
+
+def _compiled():
+    global _fast
+    if _fast is None:
+        lib()  # raises if nothing is built
+        from . import _x1cb_torch
+
+        _fast = _x1cb_torch
+    return _fast
+
+
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTS = {"none": 0, "relu": 1, "silu": 2}
 
@@ -559,6 +576,10 @@ def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str =
 
     x, r, out [B, H, W, C] float32, bfloat16 or float16; gamma, beta [C]
     float32 or None; G groups; act "none", "relu" or "silu"."""
+    if out is None and workspace is None and stream is None:
+        y = (_fast or _compiled()).norm(0, x, gamma, beta, G, eps, r, ACTS.get(act, -1), 0.0)
+        if y is not None:
+            return y
     index, shape = _norm_input(x)
     if out is None:
         out = _empty(shape, x.dtype, index, stream)
@@ -573,6 +594,10 @@ def group_norm_act_i8(x, gamma, beta, G: int, q_mul: float, eps: float = 1e-5, r
                       act: str = "relu", out=None, workspace=None, stream=None):
     """group_norm_act quantised for the int8 convolutions: clamp(rint(y * q_mul),
     -128, 127) as NC/32HW32 [B, C/32, H, W, 32]."""
+    if out is None and workspace is None and stream is None:
+        y = (_fast or _compiled()).norm(1, x, gamma, beta, G, eps, r, ACTS.get(act, -1), q_mul)
+        if y is not None:
+            return y
     index, (B, H, W, C) = _norm_input(x)
     shape = (B, C // 32, H, W, 32)
     if out is None:
@@ -603,6 +628,10 @@ def group_norm_act_mx4(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: s
                        out=None, workspace=None, stream=None):
     """group_norm_act quantised to MX4: (codes [B, H, W, C/2], scales), the
     operand of conv1x1_bias_add_act_mx4."""
+    if out is None and workspace is None and stream is None:
+        y = (_fast or _compiled()).norm(2, x, gamma, beta, G, eps, r, ACTS.get(act, -1), 0.0)
+        if y is not None:
+            return y
     index, (B, H, W, C) = _norm_input(x)
     q, sf = _mx4_outs((B, H, W), B * H * W, C, out, index, stream)
     _norm(lib().group_norm_act_mx4, "group_norm_act_mx4", x, gamma, beta, int(G), eps, r, act,
@@ -619,6 +648,10 @@ def x1cb_quantize_mx4(x, out=None, stream=None):
     """x [..., K] float32, bfloat16 or float16 -> MX4 (codes [..., K/2] uint8,
     scales [ceil(M/128), ceil(K/128), 32, 16] uint8), M the product of the
     leading sizes; K % 32 == 0."""
+    if out is None and stream is None:
+        y = (_fast or _compiled()).quantize(x)
+        if y is not None:
+            return y
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be [..., K]")
     *lead, K = x.shape
@@ -632,6 +665,10 @@ def x1cb_quantize_mx4(x, out=None, stream=None):
 
 def x1cb_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None, stream=None):
     """MX4 (codes [..., K/2], scales) -> values [..., K] of `dtype`."""
+    if out is None and stream is None:
+        y = (_fast or _compiled()).dequantize(q, sf, DTYPES.get(dtype, -1))
+        if y is not None:
+            return y
     if not isinstance(q, torch.Tensor) or q.dim() < 1:
         raise ValueError("codes must be [..., K/2]")
     *lead, half = q.shape
@@ -655,6 +692,11 @@ def conv1x1_bias_add_act_mx4(x, xs, w, ws, bias=None, r=None, act: str = "relu",
     x [B, H, W, Ic/2], xs MX4 activations; w [Oc, Ic/2], ws MX4 weights; bias
     [Oc] float32 or None; r, out [B, H, W, Oc] of `dtype` (float32, bfloat16 or
     float16)."""
+    if out is None and stream is None:
+        y = (_fast or _compiled()).conv1x1(x, xs, w, ws, bias, r, ACTS.get(act, -1),
+                                           DTYPES.get(dtype, -1))
+        if y is not None:
+            return y
     if not isinstance(x, torch.Tensor) or x.dim() != 4:
         raise ValueError("x must be [B, H, W, Ic/2]")
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
