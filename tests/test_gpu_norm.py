@@ -152,12 +152,15 @@ def test_one_outlier():
     _close(got, y, 64 * F.norm_tolerance(y, size))
 
 
-def test_constant_image():
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("shape", [(2, 33, 31, 64), (1, 500, 400, 32)])
+@pytest.mark.parametrize("value", [3.0, 1000.0, -0.0078125])
+def test_constant_image(dtype, shape, value):
     """Zero variance: every 1/std is 1/sqrt(eps), every output beta."""
-    x = torch.full((2, 33, 31, 64), 3.0, device=DEV)
-    beta = torch.arange(64, device=DEV, dtype=torch.float32)
+    x = torch.full(shape, value, device=DEV).to(dtype)
+    beta = torch.arange(shape[-1], device=DEV, dtype=torch.float32)
     got = X.group_norm_act(x, None, beta, 8, act="none")
-    assert torch.equal(got, beta.expand_as(got))
+    assert torch.equal(got, beta.to(dtype).expand_as(got))
 
 
 def test_not_a_number_and_infinity():
@@ -245,3 +248,62 @@ def test_capture_and_other_stream(shape):
     got = X.group_norm_act(x, gamma, beta, G, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_more_than_two_to_the_31_elements():
+    """Offsets pass 32 bits: the last images come out as they do alone, to a step
+    of bfloat16 (another plan may join the statistics in another order)."""
+    for shape, G in (((5600, 28, 28, 512), 32), ((11, 1024, 1024, 192), 8)):
+        x = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+        x.random_(-8, 9, generator=torch.Generator(device=DEV).manual_seed(2))
+        got = X.group_norm_act(x, None, None, G, act="none")
+        last = X.group_norm_act(x[-2:].clone(), None, None, G, act="none")
+        assert (got[-2:].float() - last.float()).abs().max() <= 2.0 ** -7 * last.float().abs().max()
+        y, size = F.group_norm(x[-1:], None, None, G, 1e-5)
+        _close(got[-1:], y, F.norm_tolerance(y, size, torch.bfloat16))
+        del x, got
+
+
+def test_own_output_and_workspace():
+    """A caller's tensors give the same bits as new ones (another way through the
+    binding), and a workspace of a byte too few is refused."""
+    for shape, G in (((3, 14, 14, 96), 3), ((1, 600, 500, 24), 4)):
+        x, gamma, beta, r = _inputs(shape, torch.float16, 21, res=True)
+        want = X.group_norm_act(x, gamma, beta, G, r=r, act="silu")
+        need = X.group_norm_workspace_size(x.dtype, *shape, G)
+        ws = torch.empty(max(need, 1), dtype=torch.int8, device=DEV)
+        out = torch.empty_like(x)
+        assert X.group_norm_act(x, gamma, beta, G, r=r, act="silu", out=out, workspace=ws) is out
+        assert torch.equal(out, want)
+        if need:
+            with pytest.raises(X.X1cbError) as e:
+                X.group_norm_act(x, gamma, beta, G, r=r, workspace=ws[:need - 1].clone())
+            assert e.value.status == X.X1CB_ERR_WORKSPACE
+
+
+def test_threads_at_once():
+    """Calls from several threads, each on its own stream and shapes."""
+    import threading
+
+    cases = [((2, 28, 28, 128), 32), ((1, 13, 17, 72), 12), ((4, 7, 7, 512), 16), ((1, 300, 200, 40), 5)]
+    data = [(_inputs(s, torch.bfloat16, 30 + i), G) for i, (s, G) in enumerate(cases)]
+    want = [X.group_norm_act(x, g, b, G, act="silu") for (x, g, b, _), G in data]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        (x, g, b, _), G = data[i]
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = X.group_norm_act(x, g, b, G, act="silu")
+            stream.synchronize()
+        if not torch.equal(got, want[i]):
+            wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

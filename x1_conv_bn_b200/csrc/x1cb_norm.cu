@@ -206,12 +206,12 @@ template <int V> struct Params {
     }
 };
 
-// The normalisation of V channels.  16-bit inputs: y = x * sc + be, be = beta -
-// mu * sc; what rounding be loses is far below the input's own step.  32-bit
-// inputs: y = (x - mu) * sc + be with the mean's low part in be.
+// The normalisation of V channels: y = (x - mu) * sc + be, with what the float mu
+// lacks of the mean in be.  (One multiply-add, x * sc + (beta - mu * sc), would
+// leave the rounding of mu * sc in y: 0.02 where a constant image of 1000 has to
+// come out as beta.)
 template <typename T, int V> struct Affine {
-    static constexpr bool kSub = sizeof(T) == 4;
-    F2 mu[kSub ? kPairs<V> : 1], sc[kPairs<V>], be[kPairs<V>];
+    F2 mu[kPairs<V>], sc[kPairs<V>], be[kPairs<V>];
     // p: gamma and beta of the channels; cs: the first of them, counted from the
     // slice's first group
     __device__ __forceinline__ Affine(const NormArgs &a, const Coef *coef, const Params<V> &p, int cs,
@@ -230,12 +230,11 @@ template <typename T, int V> struct Affine {
             s[i] = k.rstd * p.gamma[i];
             const float beta = p.beta[i];
             m[i] = -k.mu;
-            b[i] = fmaf(-k.mu_low, s[i], kSub ? beta : fmaf(-k.mu, s[i], beta));
+            b[i] = fmaf(-k.mu_low, s[i], beta);
         }
 #pragma unroll
         for (int i = 0; i < kPairs<V>; ++i) {
-            if (kSub)
-                mu[i] = f2(m[2 * i], m[2 * i + 1]);
+            mu[i] = f2(m[2 * i], m[2 * i + 1]);
             sc[i] = f2(s[2 * i], s[2 * i + 1]);
             be[i] = f2(b[2 * i], b[2 * i + 1]);
         }
@@ -246,7 +245,7 @@ template <typename T, int V> struct Affine {
         unpack<T, V>(x, y);
 #pragma unroll
         for (int i = 0; i < kPairs<V>; ++i)
-            y[i] = fma2(kSub ? add2(y[i], mu[i]) : y[i], sc[i], be[i]);
+            y[i] = fma2(add2(y[i], mu[i]), sc[i], be[i]);
         if (r) {
             F2 f[kPairs<V>];
             unpack<T, V>(*r, f);
@@ -335,7 +334,7 @@ template <typename T, int V, int OUT, bool kStream = false> struct Out {
         }
     }
     // MX4, the next kBatch pixels (n of them the thread's) at once, so that their
-    // shuffles are in flight together: thread j of a block's threads stores the
+    // shuffles are in flight together (256 x 28 x 28 x 512: 95 us one by one, 88): thread j of a block's threads stores the
     // scale of pixel j.  Whole warps call it.
     template <typename Value>
     __device__ __forceinline__ void put_batch(const NormArgs &a, int n, const Value &value)
@@ -438,7 +437,7 @@ template <typename T, int V, int OUT, bool kStream = false> struct Out {
             } else {
                 // The 32 / V neighbouring threads that hold a block agree on its scale.
                 // (With a mask of its own for each block, the shuffles of a warp run
-                // one after the other: 57 us for 128 x 28 x 28 x 512, KKK with whole
+                // one after the other: 109 us for 256 x 28 x 28 x 512, 95 with whole
                 // warps.)
                 constexpr int L = 32 / V;
                 uint32_t m = amax_bits(y);
@@ -480,7 +479,8 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
     // The last chunks first: they are the ones that the statistics left in L2.
     const int b = a.b0 + gridDim.y - 1 - blockIdx.y;
     const int p0 = (gridDim.x - 1 - blockIdx.x) * a.chunk, px = min(a.HW - p0, a.chunk);
-    // Join the chunks' statistics, in 64 bits.
+    // Join the chunks' statistics, in 64 bits and about the first chunk's mean (so
+    // that equal means join to that mean exactly).
     const int w = join_width(a.G);
     const double last = static_cast<double>(a.HW - (a.chunks - 1) * a.chunk) * a.cg;
     const double whole = static_cast<double>(a.chunk) * a.cg;
@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
         float2 kept[kKeep];
         double sum = 0., m2 = 0.;
         const int mine = g < a.G && lane < a.chunks ? (a.chunks - lane + w - 1) / w : 0;
+        const double ref = g < a.G ? part[0].x : 0.;
 #pragma unroll
         for (int j = 0; j < kKeep; ++j)
             if (j < mine)
@@ -499,11 +500,11 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
 #pragma unroll
         for (int j = 0; j < kKeep; ++j)
             if (j < mine)
-                sum += weight(j) * kept[j].x;
+                sum += weight(j) * (kept[j].x - ref);
 #pragma unroll 4
         for (int j = kKeep; j < mine; ++j)
-            sum += weight(j) * part[static_cast<size_t>(lane + j * w) * a.G].x;
-        const double mean = lanes_sum(sum, w) * a.inv_count;
+            sum += weight(j) * (part[static_cast<size_t>(lane + j * w) * a.G].x - ref);
+        const double mean = ref + lanes_sum(sum, w) * a.inv_count;
 #pragma unroll
         for (int j = 0; j < kKeep; ++j)
             if (j < mine)
@@ -676,7 +677,8 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
                              : "memory");
                 n = static_cast<double>(max(0, min(a.HW - q * share, share))) * a.cg;
             }
-            const double mean = lanes_sum(n * m, 8) * a.inv_count;
+            const double ref = __shfl_sync(0xffffffffu, m, 0, 8);  // (rank 0 has pixels)
+            const double mean = ref + lanes_sum(n * (m - ref), 8) * a.inv_count;
             const double m2 = lanes_sum(n > 0. ? v + n * (m - mean) * (m - mean) : 0., 8);
             if (g < groups && q == 0)
                 coef[g] = make_coef(Joined{mean, m2}, a.inv_count, a.eps);
