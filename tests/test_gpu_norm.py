@@ -250,6 +250,17 @@ def test_capture_and_other_stream(shape):
     assert torch.equal(got, want)
 
 
+def test_many_chunks():
+    """An image of more than 128 chunks: the statistics are joined by a launch of
+    their own.  The data lies far from zero, in each channel elsewhere."""
+    for dtype, shape, G in ((torch.bfloat16, (2, 700, 513, 128), 32), (torch.float32, (1, 999, 1001, 36), 3)):
+        x, gamma, beta, _ = _inputs(shape, dtype, 40, mean=torch.arange(shape[-1], device=DEV) / 4.0)
+        y, size = F.group_norm(x, gamma, beta, G, 1e-5)
+        got = X.group_norm_act(x, gamma, beta, G, act="none")
+        _close(got, y, F.norm_tolerance(y, size, dtype))
+        assert torch.equal(got, X.group_norm_act(x, gamma, beta, G, act="none"))
+
+
 def test_more_than_two_to_the_31_elements():
     """Offsets pass 32 bits: the last images come out as they do alone, to a step
     of bfloat16 (another plan may join the statistics in another order)."""

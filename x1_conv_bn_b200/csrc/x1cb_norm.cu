@@ -16,7 +16,8 @@
 // reads it once, keeps it there, joins the statistics over the cluster and
 // normalises from shared memory: x in, y out, nothing else.  Larger images take
 // two launches, partial statistics per chunk of pixels into the workspace and
-// the normalisation, over as many images at a time as stay in L2 between them.
+// the normalisation, over as many images at a time as stay in L2 between them (and
+// one between the two that joins the chunks, where there are many).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -37,12 +38,18 @@ constexpr int kBlock = 256;
 constexpr int kFold = 64;  // pixels a thread's shifted sums run over at most
 constexpr int kBatch = 4;  // vectors a thread has in flight
 
+// What the normalisation needs of a group.
+struct Coef {
+    float mu, mu_low, rstd;  // the mean as a float and that float's rounding error
+};
+
 struct NormArgs {
     const void *x, *r;
     const float *gamma, *beta;
     void *y;
     uint8_t *sf;
     float2 *part;  // [B][chunks][G] (mean, M2)
+    Coef *coef;    // [B][G], where a launch of its own joins the chunks (else NULL)
     float eps, q_mul;
     int act, B, HW, C, G, cg;
     int nv;             // vectors of V channels per pixel
@@ -173,10 +180,6 @@ __device__ __forceinline__ int join_width(int groups)
     return w;
 }
 
-// What the normalisation needs of a group.
-struct Coef {
-    float mu, mu_low, rstd;  // the mean as a float and that float's rounding error
-};
 __device__ __forceinline__ Coef make_coef(const Joined &j, double inv_count, float eps)
 {
     Coef c;
@@ -301,6 +304,46 @@ template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stat
         if (g < a.G && threadIdx.x % w == 0)
             a.part[(static_cast<size_t>(b) * a.chunks + blockIdx.x) * a.G + g] =
                 make_float2(static_cast<float>(r.mean), static_cast<float>(r.m2));
+    }
+}
+
+// Joins the chunks' statistics in a launch of its own, a block per group of an
+// image, where there are so many of them that each block of the normalisation
+// should not repeat it.  In 64 bits and about the first chunk's mean R (equal means
+// join to that mean exactly): S1 = sum n (mean - R), S2 = sum M2 + n (mean - R)^2.
+__global__ void __launch_bounds__(kBlock) norm_join_kernel(NormArgs a)
+{
+    __shared__ double sums[2][kBlock / 32];
+    griddep_wait();
+    const int g = blockIdx.x, b = a.b0 + blockIdx.y;
+    const float2 *part = a.part + static_cast<size_t>(b) * a.chunks * a.G + g;
+    const double last = static_cast<double>(a.HW - (a.chunks - 1) * a.chunk) * a.cg;
+    const double whole = static_cast<double>(a.chunk) * a.cg;
+    const double ref = part[0].x;
+    double s1 = 0., s2 = 0.;
+#pragma unroll 4
+    for (int j = threadIdx.x; j < a.chunks; j += kBlock) {
+        const float2 p = part[static_cast<size_t>(j) * a.G];
+        const double n = j == a.chunks - 1 ? last : whole, e = p.x - ref;
+        s1 += n * e;
+        s2 += p.y + n * e * e;
+    }
+    s1 = lanes_sum(s1, 32);
+    s2 = lanes_sum(s2, 32);
+    if (threadIdx.x % 32 == 0) {
+        sums[0][threadIdx.x / 32] = s1;
+        sums[1][threadIdx.x / 32] = s2;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s1 = s2 = 0.;
+        for (int i = 0; i < kBlock / 32; ++i) {
+            s1 += sums[0][i];
+            s2 += sums[1][i];
+        }
+        const double off = s1 * a.inv_count, m2 = s2 - s1 * off;
+        a.coef[static_cast<size_t>(b) * a.G + g] =
+            make_coef(Joined{ref + off, m2 < 0. ? 0. : m2}, a.inv_count, a.eps);  // (NaN stays)
     }
 }
 
@@ -479,44 +522,49 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
     // The last chunks first: they are the ones that the statistics left in L2.
     const int b = a.b0 + gridDim.y - 1 - blockIdx.y;
     const int p0 = (gridDim.x - 1 - blockIdx.x) * a.chunk, px = min(a.HW - p0, a.chunk);
-    // Join the chunks' statistics, in 64 bits and about the first chunk's mean (so
-    // that equal means join to that mean exactly).
-    const int w = join_width(a.G);
-    const double last = static_cast<double>(a.HW - (a.chunks - 1) * a.chunk) * a.cg;
-    const double whole = static_cast<double>(a.chunk) * a.cg;
-    for (int g0 = 0; g0 < a.G; g0 += kBlock / w) {
-        const int g = g0 + threadIdx.x / w, lane = threadIdx.x & (w - 1);
-        const float2 *part = a.part + static_cast<size_t>(b) * a.chunks * a.G + g;
-        constexpr int kKeep = 8;  // parts a lane holds from the first pass to the second
-        float2 kept[kKeep];
-        double sum = 0., m2 = 0.;
-        const int mine = g < a.G && lane < a.chunks ? (a.chunks - lane + w - 1) / w : 0;
-        const double ref = g < a.G ? part[0].x : 0.;
+    if (a.coef) {
+        for (int g = threadIdx.x; g < a.G; g += kBlock)
+            coef[g] = a.coef[static_cast<size_t>(b) * a.G + g];
+    } else {
+        // Join the chunks, in 64 bits and about the first one's mean (so that equal
+        // means join to that mean exactly).
+        const int w = join_width(a.G);
+        const double last = static_cast<double>(a.HW - (a.chunks - 1) * a.chunk) * a.cg;
+        const double whole = static_cast<double>(a.chunk) * a.cg;
+        for (int g0 = 0; g0 < a.G; g0 += kBlock / w) {
+            const int g = g0 + threadIdx.x / w, lane = threadIdx.x & (w - 1);
+            const float2 *part = a.part + static_cast<size_t>(b) * a.chunks * a.G + g;
+            constexpr int kKeep = 8;  // parts a lane holds from the first pass to the second
+            float2 kept[kKeep];
+            double sum = 0., m2 = 0.;
+            const int mine = g < a.G && lane < a.chunks ? (a.chunks - lane + w - 1) / w : 0;
+            const double ref = g < a.G ? part[0].x : 0.;
 #pragma unroll
-        for (int j = 0; j < kKeep; ++j)
-            if (j < mine)
-                kept[j] = part[static_cast<size_t>(lane + j * w) * a.G];
-        const auto weight = [&](int j) { return lane + j * w == a.chunks - 1 ? last : whole; };
+            for (int j = 0; j < kKeep; ++j)
+                if (j < mine)
+                    kept[j] = part[static_cast<size_t>(lane + j * w) * a.G];
+            const auto weight = [&](int j) { return lane + j * w == a.chunks - 1 ? last : whole; };
 #pragma unroll
-        for (int j = 0; j < kKeep; ++j)
-            if (j < mine)
-                sum += weight(j) * (kept[j].x - ref);
+            for (int j = 0; j < kKeep; ++j)
+                if (j < mine)
+                    sum += weight(j) * (kept[j].x - ref);
 #pragma unroll 4
-        for (int j = kKeep; j < mine; ++j)
-            sum += weight(j) * (part[static_cast<size_t>(lane + j * w) * a.G].x - ref);
-        const double mean = ref + lanes_sum(sum, w) * a.inv_count;
+            for (int j = kKeep; j < mine; ++j)
+                sum += weight(j) * (part[static_cast<size_t>(lane + j * w) * a.G].x - ref);
+            const double mean = ref + lanes_sum(sum, w) * a.inv_count;
 #pragma unroll
-        for (int j = 0; j < kKeep; ++j)
-            if (j < mine)
-                m2 += kept[j].y + weight(j) * (kept[j].x - mean) * (kept[j].x - mean);
+            for (int j = 0; j < kKeep; ++j)
+                if (j < mine)
+                    m2 += kept[j].y + weight(j) * (kept[j].x - mean) * (kept[j].x - mean);
 #pragma unroll 4
-        for (int j = kKeep; j < mine; ++j) {
-            const float2 p = part[static_cast<size_t>(lane + j * w) * a.G];
-            m2 += p.y + weight(j) * (p.x - mean) * (p.x - mean);
+            for (int j = kKeep; j < mine; ++j) {
+                const float2 p = part[static_cast<size_t>(lane + j * w) * a.G];
+                m2 += p.y + weight(j) * (p.x - mean) * (p.x - mean);
+            }
+            m2 = lanes_sum(m2, w);
+            if (g < a.G && lane == 0)
+                coef[g] = make_coef(Joined{mean, m2}, a.inv_count, a.eps);
         }
-        m2 = lanes_sum(m2, w);
-        if (g < a.G && lane == 0)
-            coef[g] = make_coef(Joined{mean, m2}, a.inv_count, a.eps);
     }
     if (OUT == kNormMx4 && b == 0 && blockIdx.x == 0)
         mx4_zero_row_padding(a.sf, static_cast<long long>(a.B) * a.HW, (a.C + 127) / 128,
@@ -746,6 +794,7 @@ int vector_channels(int dtype, int n)
 struct Plan {
     int V, nv, lanes;
     int chunks, chunk, images;            // two-launch form: per image; images at a time
+    int joined;                           // the chunks are joined in a launch of their own
     int cluster, Cs, slices, iters, smem;  // cluster form (cluster = 0: two launches)
     int stage_r;
 };
@@ -839,6 +888,9 @@ Plan search_plan(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool
     p.chunks = static_cast<int>(std::min(want, most));
     p.chunk = std::min((HW + p.chunks - 1) / p.chunks, kFold * p.lanes);
     p.chunks = (HW + p.chunk - 1) / p.chunk;
+    // (of 32 groups: 37 chunks 33.0 us joined by every block, 33.5 in a launch of
+    // its own; 296 chunks 49.0 and 42.6, 8192 8974 and 1129)
+    p.joined = p.chunks > 128;
     return p;
 }
 
@@ -925,6 +977,10 @@ int run(const NormCall &c, const Plan &p, NormArgs a, cudaStream_t s)
         const dim3 grid(p.chunks, std::min(p.images, c.B - a.b0));
         if (int e = launch(ks, grid, static_cast<size_t>(p.lanes) * c.C * sizeof(float2), 1, s, a))
             return e;
+        if (p.joined)
+            if (int e = launch(reinterpret_cast<const void *>(norm_join_kernel), dim3(c.G, grid.y), 0, 1,
+                               s, a))
+                return e;
         if (int e = launch(ka, grid, static_cast<size_t>(c.G) * sizeof(Coef), 1, s, a))
             return e;
     }
@@ -956,6 +1012,8 @@ int run_v(const NormCall &c, const Plan &p, const NormArgs &a, cudaStream_t s)
 
 }  // namespace
 
+constexpr int kCoefFloats = sizeof(Coef) / sizeof(float);
+
 // The workspace does not depend on the output's form: the larger of the two.
 size_t norm_workspace_floats(int dtype, int B, int HW, int C, int G)
 {
@@ -963,7 +1021,7 @@ size_t norm_workspace_floats(int dtype, int B, int HW, int C, int G)
     for (int whole = 0; whole <= (C % 32 == 0 ? 1 : 0); ++whole) {
         const Plan p = plan_norm(dtype, B, HW, C, G, whole != 0, false);
         if (!p.cluster)
-            n = std::max(n, static_cast<size_t>(B) * p.chunks * G * 2);
+            n = std::max(n, static_cast<size_t>(B) * G * (static_cast<size_t>(p.chunks) * 2 + p.joined * kCoefFloats));
     }
     return n;
 }
@@ -979,6 +1037,8 @@ int launch_norm(const NormCall &c, cudaStream_t s)
     a.y = c.y;
     a.sf = c.sf;
     a.part = reinterpret_cast<float2 *>(c.ws);
+    if (p.joined)
+        a.coef = reinterpret_cast<Coef *>(a.part + static_cast<size_t>(c.B) * p.chunks * c.G);
     a.eps = c.eps;
     a.q_mul = c.q_mul;
     a.act = c.act;
