@@ -353,7 +353,7 @@ int group_norm_act_mx4(const void *x, int dtype, const float *gamma, const float
                        void *stream);
 
 /* Bytes of the scales of an [M, K] MX4 matrix: ceil(M/128)*ceil(K/128)*512
- * (0 for a negative size). */
+ * (0 for a negative size or M > 2^31 - 1). */
 size_t x1cb_mx4_scale_size(long long M, int K);
 
 /*
@@ -361,7 +361,7 @@ size_t x1cb_mx4_scale_size(long long M, int K);
  * 127, 0, 254) (0 for a block of zeros); code = x * 2^(127 - s) rounded to the
  * nearest e2m1 value, ties to the even code, at most +-6.  A block that holds
  * an infinity or a NaN gets s = 255 and zero codes: its 32 values read back as
- * NaN.  K % 32 == 0, M <= 2^31 - 1.
+ * NaN.  K % 32 == 0, M <= 2^31 - 256.
  */
 int x1cb_quantize_mx4(const void *x, int dtype, uint8_t *q, uint8_t *sf, long long M, int K,
                       void *stream);
@@ -378,7 +378,7 @@ int x1cb_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtype,
  *   x [B*H*W, Ic/2], xs  MX4 activations (read); w [Oc, Ic/2], ws MX4 weights
  *   (read); bias [Oc] float or NULL; r [B, H, W, Oc] of `dtype` or NULL;
  *   out [B, H, W, Oc] of `dtype` (written).
- * Ic % 32 == 0, Ic <= 65536; 1 <= Oc <= 65536; B*H*W <= 2^31 - 1.
+ * Ic % 32 == 0, Ic <= 65536; 1 <= Oc <= 65536; B*H*W <= 2^31 - 256.
  */
 int conv1x1_bias_add_act_mx4(const uint8_t *x, const uint8_t *xs, const uint8_t *w,
                              const uint8_t *ws, const float *bias, const void *r, int act,

@@ -81,7 +81,7 @@ def test_conversion_refusals(L, back):
             return L.x1cb_dequantize_mx4(_p(q), _p(sf), _p(x), dtype, M, K, None)
         return L.x1cb_quantize_mx4(_p(x), dtype, _p(q), _p(sf), M, K, None)
 
-    for bad in (dict(dtype=3), dict(M=-1), dict(M=1 << 31), dict(K=0), dict(K=16), dict(K=-32),
+    for bad in (dict(dtype=3), dict(M=-1), dict(M=1 << 31), dict(M=(1 << 31) - 255), dict(K=0), dict(K=16), dict(K=-32),
                 dict(K=65568)):
         assert call(**bad) == X.X1CB_ERR_SHAPE, bad
     for bad in (dict(x=0), dict(q=0), dict(sf=0)):
@@ -101,6 +101,8 @@ def test_scale_size(L):
     assert X.x1cb_mx4_scale_size(1, 32) == 512
     assert X.x1cb_mx4_scale_size(129, 160) == 2 * 2 * 512
     assert X.x1cb_mx4_scale_size(-1, 32) == 0
+    for M in (1 << 31, (1 << 63) - 1):
+        assert X.x1cb_mx4_scale_size(M, 32) == 0
     assert X.x1cb_mx4_scale_size((1 << 31) - 1, 65536) == (1 << 24) * 512 * 512
 
 
@@ -112,7 +114,7 @@ def test_conv_refusals(L):
 
     for bad in (dict(dtype=7), dict(act=9), dict(B=-1), dict(H=-1), dict(W=-1), dict(Ic=48),
                 dict(Ic=0), dict(Ic=65568), dict(Oc=0), dict(Oc=65537), dict(H=65536, W=65536),
-                dict(B=3, H=32768, W=32768)):
+                dict(B=3, H=32768, W=32768), dict(B=1, H=(1 << 31) - 255, W=1)):
         assert call(**bad) == X.X1CB_ERR_SHAPE, bad
     for bad in (dict(x=0), dict(xs=0), dict(w=0), dict(ws=0), dict(out=0)):
         assert call(**bad) == X.X1CB_ERR_NULL, bad
@@ -146,3 +148,23 @@ def test_binding_refusals():
         X.x1cb_dequantize_mx4(q, torch.zeros(1, 1, 32, 4, dtype=torch.uint8))
     with pytest.raises(ValueError):
         X.conv1x1_bias_add_act_mx4(q, None, torch.zeros(8, 32, dtype=torch.uint8), None)
+
+
+def test_marshalling_module_leaves_the_unusual_alone():
+    """The compiled marshalling answers None (the Python way then says what is
+    wrong) to anything but plain CUDA tensors; no call here has a device."""
+    from x1_conv_bn_b200 import _build
+
+    _build.build()
+    f = X._compiled()
+    x, q = torch.zeros(1, 2, 2, 32), torch.zeros(1, 2, 2, 16, dtype=torch.uint8)
+    s = torch.zeros(1, 1, 32, 16, dtype=torch.uint8)
+    assert f.norm(0, x, None, None, 4, 1e-5, None, 1, 0.0) is None
+    assert f.norm(0, None, None, None, 4, 1e-5, None, 1, 0.0) is None
+    assert f.norm(0, x, None, None, "4", 1e-5, None, 1, 0.0) is None
+    assert f.norm(0, x) is None
+    assert f.quantize(x) is None and f.quantize(3) is None and f.quantize(x, x) is None
+    assert f.dequantize(q, s, 1) is None and f.dequantize(q, s, -1) is None
+    assert f.dequantize(q, s, "bf16") is None
+    assert f.conv1x1(q, s, q, s, None, None, 1, 1) is None
+    assert f.conv1x1(q, s, q, s, None, None, -1, 7) is None

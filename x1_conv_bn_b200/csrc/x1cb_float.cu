@@ -64,9 +64,10 @@ int norm_common(NormCall c, size_t ws_bytes, int H, int W, void *stream)
     return launch_norm(c, static_cast<cudaStream_t>(stream));
 }
 
+// (256 rows short of 2^31: the kernels count rows of whole tiles in an int)
 int check_mx4_shape(long long M, int K)
 {
-    return M < 0 || M > INT_MAX || K < 32 || K % 32 || K > 65536 ? X1CB_ERR_SHAPE : X1CB_OK;
+    return M < 0 || M > INT_MAX - 255 || K < 32 || K % 32 || K > 65536 ? X1CB_ERR_SHAPE : X1CB_OK;
 }
 
 // Shared by the two conversions; `values_out`: x is the output.
@@ -137,7 +138,7 @@ int group_norm_act_mx4(const void *x, int dtype, const float *gamma, const float
 
 size_t x1cb_mx4_scale_size(long long M, int K)
 {
-    if (M < 0 || K < 0)
+    if (M < 0 || M > INT_MAX || K < 0)
         return 0;
     return static_cast<size_t>((M + 127) / 128) * ((K + 127LL) / 128) * 512;
 }
