@@ -197,6 +197,26 @@ def test_conv_exact(shape):
     assert torch.equal(got.view(M, Oc).double(), xv @ wv.T)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("shape", [(41, 21, 23, 96, 52), (41, 21, 23, 96, 131), (41, 21, 23, 32, 250),
+                                   (1, 1, 77, 512, 445), (40, 16, 16, 1024, 1001),
+                                   (40, 16, 16, 1024, 1002), (1, 1, 65, 64, 1)])
+def test_conv_rows_off_16_bytes(shape, dtype):
+    """Rows of no multiple of 16 bytes, several tiles to a CTA, with a shortcut;
+    and the elements behind the last row are left as they were."""
+    _conv(shape, dtype, "relu", True, True, sum(shape))
+    _conv(shape, dtype, "none", False, False, sum(shape))
+    B, H, W, Ic, Oc = shape
+    g, M = _gen(7), B * H * W
+    (x, xs), _ = _operand(M, Ic, g)
+    (w, ws), _ = _operand(Oc, Ic, g)
+    buf = torch.full((M * Oc + 64,), 7.0, dtype=dtype, device=DEV)
+    out = buf[:M * Oc].view(B, H, W, Oc)
+    X.conv1x1_bias_add_act_mx4(x.view(B, H, W, Ic // 2), xs, w, ws, dtype=dtype, out=out)
+    _clean()
+    assert (buf[M * Oc:] == 7.0).all()
+
+
 def test_conv_row_masks():
     """Zero rows, and blocks whose scale is NaN: their row (or channel) alone is NaN."""
     g = _gen(5)

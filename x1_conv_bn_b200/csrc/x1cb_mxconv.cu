@@ -164,6 +164,26 @@ template <int kAccs> struct Turn {
     }
 };
 
+// A load whose result stays as it came, in whole registers, until it is used: the
+// parts of a 4-byte or the value of a 2-byte Vec would be taken out at once, each
+// load waiting for the one before (200000 x 64 x 250 with a shortcut: 154 us, 66 so).
+template <int BYTES> struct Late {
+    using type = typename Raw<BYTES>::type;
+    static __device__ __forceinline__ type load(const void *p)
+    {
+        return __ldg(static_cast<const type *>(p));
+    }
+};
+template <> struct Late<2> {
+    using type = uint32_t;
+    static __device__ __forceinline__ type load(const void *p)
+    {
+        uint32_t v;
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(v) : "l"(p));
+        return v;
+    }
+};
+
 // kIo: outputs (and the shortcut) move as 128 x 128-byte boxes by TMA, which
 // needs rows of a multiple of 16 bytes; otherwise the plain epilogue transposes
 // through shared memory and stores element by element.
@@ -586,40 +606,120 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
                     release(acc_empty(acc));
             }
         } else {
-            float *patch = reinterpret_cast<float *>(smem) + e * (kPatch / 4);
-            constexpr int kParts = BN / 64;  // of 64 columns, 32 for each side
-            for (Tiles t(a, unit + group * units, S::kGroups * units); !t.done() && wait_acc();
-                 t.next(), turn.next(S::kGroups)) {
-                const int acc = turn.acc;
-                const long long row0 = static_cast<long long>(t.mt) * (kPair ? 256 : 128) + row_off;
-                const int rows = static_cast<int>(max(0ll, min(32ll, a.M - row0)));
-                for (int part = 0; part < kParts; ++part) {
-                    // the shared columns first
-                    const int c0 = (acc ? part : kParts - 1 - part) * 64 + side * 32;
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32_sync(lanes_at + acc * S::kSecond + c0, v);
-                    if (kPair && part == S::kSharedCols / 64 - 1)
-                        release(shared_free);
+            // Parts of 64 columns, 32 for each side: accumulator -> patch -> rows, in
+            // turns of 8 V rows in which a lane takes V neighbouring columns of
+            // every V-th row.  The shortcut of a turn is loaded while the one before it
+            // is worked on (140800 x 96 x 52 with one: 79.8 us without that, 27.0 so),
+            // the bias of a part likewise.  The turns are a loop of few instructions:
+            // unrolled, fetching them took longer than the work.
+            const auto plain = [&](auto vec) {
+                constexpr int V = decltype(vec)::value, kParts = BN / 64, kRows = 8;
+                constexpr int kTurn = kRows * V;  // rows a turn
+                float *patch = reinterpret_cast<float *>(smem) + e * (kPatch / 4);
+                const int lr = lane / (32 / V), lc = lane % (32 / V) * V;
+                const size_t step = static_cast<size_t>(V) * a.N;
+                struct Part {
+                    size_t at;  // the lane's first element
+                    int rows;   // rows from there on, counted in steps of V
+                    float bias[V];
+                };
+                const auto part_at = [&](const Tiles &t, int acc, int part) {
+                    Part p;
+                    // (accumulator 0 shares its last columns with the next tile's first)
+                    const int c = t.nt * BN + (acc ? part : kParts - 1 - part) * 64 + side * 32 + lc;
+                    const long long row =
+                        static_cast<long long>(t.mt) * (kPair ? 256 : 128) + row_off + lr;
+                    p.rows = t.done() || c >= a.N
+                                 ? 0
+                                 : static_cast<int>(max(0ll, min(32ll - lr, a.M - row)));
+                    p.at = static_cast<size_t>(row) * a.N + c;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        patch[lane * 33 + i] = __uint_as_float(v[i]);
-                    __syncwarp();
-                    const int o = t.nt * BN + c0 + lane;
-                    if (o < a.N) {
-                        const float b = a.bias ? a.bias[o] : 0.f;
-                        size_t at = static_cast<size_t>(row0) * a.N + o;
-#pragma unroll 4
-                        for (int i = 0; i < rows; ++i, at += a.N) {
-                            float y = patch[i * 33 + lane] + b;
-                            if (a.r)
-                                y += to_f(static_cast<const T *>(a.r)[at]);
-                            static_cast<T *>(a.out)[at] = from_f<T>(activate(y, a.act));
-                        }
+                    for (int i = 0; i < V; ++i)
+                        p.bias[i] = a.bias && p.rows > 0 ? __ldg(a.bias + c + i) : 0.f;
+                    return p;
+                };
+                using L = Late<sizeof(T) * V>;
+                typename L::type rv[kRows];
+                const auto load_r = [&](size_t at, int rows) {
+                    if (a.r) {
+                        const T *r = static_cast<const T *>(a.r) + at;
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i)
+                            if (i * V < rows)
+                                rv[i] = L::load(r + i * step);
                     }
-                    __syncwarp();
+                };
+                Tiles t(a, unit + group * units, S::kGroups * units);
+                Part next = part_at(t, turn.acc, 0);
+                load_r(next.at, next.rows);
+                while (!t.done() && wait_acc()) {
+                    const int acc = turn.acc;
+                    const Tiles now = t;
+                    t.next();
+                    turn.next(S::kGroups);
+#pragma unroll 1
+                    for (int part = 0; part < kParts; ++part) {
+                        const int c0 = (acc ? part : kParts - 1 - part) * 64 + side * 32;
+                        const bool last = part == kParts - 1, any = now.nt * BN + c0 < a.N;
+                        if (any) {
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32_sync(lanes_at + acc * S::kSecond + c0, v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                patch[lane * 33 + i] = __uint_as_float(v[i]);
+                        }
+                        if (kPair && part == S::kSharedCols / 64 - 1)
+                            release(shared_free);
+                        if (last)
+                            release(acc_empty(acc));
+                        const Part p = next;
+                        next = part_at(last ? t : now, last ? turn.acc : acc, last ? 0 : part + 1);
+                        __syncwarp();
+                        size_t at = p.at;
+                        const float *from = patch + lr * 33 + lc;
+                        for (int row = any ? 0 : 32; row < 32; row += kTurn) {
+                            float y[kTurn];
+#pragma unroll
+                            for (int i = 0; i < kTurn; ++i)
+                                y[i] = from[i / V * V * 33 + i % V] + p.bias[i % V];
+                            if (a.r) {
+#pragma unroll
+                                for (int i = 0; i < kRows; ++i) {
+                                    F2 f[1];
+                                    unpack<T, V>(*reinterpret_cast<const Vec<T, V> *>(&rv[i]), f);
+                                    y[i * V] += un2(f[0]).x;
+                                    if (V == 2)
+                                        y[i * V + V - 1] += un2(f[0]).y;
+                                }
+                                const bool more = row + kTurn < 32;
+                                load_r(more ? at + kRows * step : next.at,
+                                       more ? p.rows - row - kTurn : next.rows);
+                            }
+                            activate(y, a.act);
+                            T *to = static_cast<T *>(a.out) + at;
+#pragma unroll
+                            for (int i = 0; i < kRows; ++i) {
+                                if (row + i * V < p.rows) {
+                                    Vec<T, V> w;
+#pragma unroll
+                                    for (int k = 0; k < V; ++k)
+                                        w.e[k] = from_f<T>(y[i * V + k]);
+                                    store_vec<T, V>(to + i * step, w);
+                                }
+                            }
+                            at += kRows * step;
+                            from += kTurn * 33;
+                        }
+                        if (!any)
+                            load_r(next.at, next.rows);
+                        __syncwarp();
+                    }
                 }
-                release(acc_empty(acc));
-            }
+            };
+            if (a.N % 2 == 0)
+                plain(std::integral_constant<int, 2>{});
+            else
+                plain(std::integral_constant<int, 1>{});
         }
         __syncwarp();
     }
@@ -680,6 +780,10 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
     const int epi = ((kIo ? 2 * S::kGroups * a.io * kIoBox : S::kEpiWarps * kPatch) + 1023) & ~1023;
     const int fixed = 1024 + epi + static_cast<int>(sizeof(Tail));
     a.stages = std::min({(232448 - fixed) / S::kStage, S::kSfStages, 8});
+    // The plain epilogue's loads need L1: 200000 x 64 x 250 with a shortcut 66.0 us
+    // with all of the shared memory taken by the ring, 61.5 with half of it.
+    if (!kIo && c.r)
+        a.stages = std::min(a.stages, std::max(2, (110 * 1024 - fixed) / S::kStage));
     const int smem = fixed + a.stages * S::kStage;
 
     CUtensorMap tmX, tmW, tmXs, tmWs, tmR, tmO;
