@@ -197,6 +197,17 @@ def test_conv_exact(shape):
     assert torch.equal(got.view(M, Oc).double(), xv @ wv.T)
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 64, 1024, 512), (1, 1, 65, 2400, 384), (2, 1, 50, 1280, 130),
+                                   (1, 14, 14, 4096, 1000), (1, 16, 16, 4096, 48), (3, 16, 16, 4096, 48),
+                                   (1, 1, 2, 1280, 77), (1, 1, 33, 800, 2048), (1, 1, 40, 4096, 2049),
+                                   (1, 1, 64, 4096, 8200)])
+def test_conv_split_over_clusters(shape):
+    """Few rows, or few tiles and a long K: every split of K, CTAs whose share of
+    it is empty among them, and units whose last rows or channels are missing."""
+    _conv(shape, torch.float32, "none", True, True, sum(shape))
+    _conv(shape, torch.bfloat16, "silu", False, False, sum(shape))
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("shape", [(41, 21, 23, 96, 52), (41, 21, 23, 96, 131), (41, 21, 23, 32, 250),
                                    (1, 1, 77, 512, 445), (40, 16, 16, 1024, 1001),

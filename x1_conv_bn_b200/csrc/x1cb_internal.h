@@ -118,5 +118,6 @@ struct Mx4Call {
 int launch_conv_mx4(const Mx4Call &c, cudaStream_t s);
 int launch_conv_mx4_tiles(const Mx4Call &c, cudaStream_t s);  // x1cb_mxconv.cu
 int launch_conv_mx4_split(const Mx4Call &c, cudaStream_t s);  // x1cb_mxsplit.cu
+bool conv_mx4_split_pays(const Mx4Call &c);  // (of a call with more than 64 rows)
 
 }  // namespace x1cb

@@ -340,12 +340,12 @@ int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtyp
     return launch(k, dim3(blocks_for(c, 32)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
 }
 
-// One row: conv_row_kernel.  Up to 64: the weights as the MMA's rows, K split
-// over clusters (4096 x 4096: 16 rows 5.3 us, 64 rows 8.2 us, against 9.9 with
-// 128-row tiles; 128 rows 10.6 against 10.2).  More: 128-row tiles.
+// One row: conv_row_kernel.  Up to 64, and a few more where K is long: the weights
+// as the MMA's rows, K split over clusters (4096 x 4096: 16 rows 5.3 us, 64 rows 8.2
+// us, against 9.9 with 128-row tiles).  More: 128-row tiles.
 int launch_conv_mx4(const Mx4Call &c, cudaStream_t s)
 {
-    if (c.M > 64)
+    if (c.M > 64 && !conv_mx4_split_pays(c))
         return launch_conv_mx4_tiles(c, s);
     if (c.M > 1)
         return launch_conv_mx4_split(c, s);

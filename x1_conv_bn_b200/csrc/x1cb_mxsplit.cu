@@ -13,9 +13,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "x1cb_float.cuh"
 #include "x1cb_internal.h"
@@ -300,12 +300,91 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
 }
 
-template <typename T, int NB> int run(const Mx4Call &c, int sms, cudaStream_t s)
-{
+// What a launch of the kernel needs to know once per device: its shared memory,
+// opted in to, and how many clusters of 8 and of 4 CTAs the chip holds at once (a
+// cluster lies within a GPC, so 8 x 16 CTAs are more than 148 SMs hold).
+struct Fit {
+    int of8, of4;
+};
+template <typename T, int NB> struct Kernel {
     using S = SplitShape<NB>;
+    static constexpr int kSmem =
+        1024 + S::kStages * S::kStage + S::kPart + static_cast<int>(sizeof(SplitTail));
+    static_assert(kSmem > 114 * 1024, "two of these kernels would share an SM");
+
+    static int prepare(Fit &fit)
+    {
+        static std::mutex mu;
+        static Fit known[64];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+            return X1CB_ERR_CUDA;
+        std::lock_guard<std::mutex> lk(mu);
+        if (!known[dev].of4) {
+            const auto kern = conv_mx4_split_kernel<T, NB>;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+                cudaSuccess)
+                return X1CB_ERR_CUDA;
+            Fit f{};
+            for (int split = 8; split >= 4; split /= 2) {
+                cudaLaunchConfig_t cfg;
+                cudaLaunchAttribute attr[2];
+                configure(cfg, attr, 148 / split, split, nullptr);
+                if (cudaOccupancyMaxActiveClusters(split == 8 ? &f.of8 : &f.of4, kern, &cfg) !=
+                    cudaSuccess)
+                    return X1CB_ERR_CUDA;
+            }
+            if (!f.of4)
+                return X1CB_ERR_CUDA;
+            known[dev] = f;
+        }
+        fit = known[dev];
+        return X1CB_OK;
+    }
+    static void configure(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, long long units, int split,
+                          cudaStream_t s)
+    {
+        std::memset(&cfg, 0, sizeof(cfg));
+        cfg.gridDim = dim3(static_cast<unsigned>(units * split), 1, 1);
+        cfg.blockDim = dim3(kSplitThreads, 1, 1);
+        cfg.dynamicSmemBytes = kSmem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = split;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = split > 1 ? 2 : 1;
+    }
+};
+
+long long units_of(const Mx4Call &c, int NB)
+{
+    return (c.M + NB - 1) / NB * ((c.N + 127) / 128);
+}
+
+// CTAs to split K over.  64 x 4096 x 1792: 10.6 us with one, 10.3 with two, 7.9 with
+// four, 6.9 with eight; 64 x 4096 x 2048, whose 16 clusters of eight do not run at
+// once, 13.0 with eight, 7.9 with four; 64 x 1024 x 512 7.2, 8.6, 7.0, 6.5.
+int split_for(long long units, int k_steps, const Fit &fit)
+{
+    return k_steps >= 4 && units <= fit.of8   ? 8
+           : k_steps >= 4 && units <= fit.of4 ? 4
+           : k_steps >= 16 && units <= 74     ? 2
+                                              : 1;
+}
+
+template <typename T, int NB> int run(const Mx4Call &c, cudaStream_t s)
+{
+    using Ke = Kernel<T, NB>;
     SplitArgs a{};
     unsigned int *forms = nullptr;
     if (int e = device_words(&a.status, &forms))
+        return e;
+    Fit fit;
+    if (int e = Ke::prepare(fit))
         return e;
     a.bias = c.bias;
     a.r = c.r;
@@ -319,10 +398,8 @@ template <typename T, int NB> int run(const Mx4Call &c, int sms, cudaStream_t s)
     a.k_steps = (c.K + 255) / 256;
     a.ch_tiles = (c.N + 127) / 128;
     const int kt = (c.K + 127) / 128;
-    const long long units = static_cast<long long>((c.M + NB - 1) / NB) * a.ch_tiles;
-    int split = 1;
-    while (split < 8 && split < a.k_steps && units * split * 2 <= sms)
-        split *= 2;
+    const long long units = units_of(c, NB);
+    const int split = split_for(units, a.k_steps, fit);
     a.per = (a.k_steps + split - 1) / split;
     CUtensorMap tmX, tmW, tmXs, tmWs;
     const uint64_t str[1] = {static_cast<uint64_t>(c.K) / 2};
@@ -343,55 +420,42 @@ template <typename T, int NB> int run(const Mx4Call &c, int sms, cudaStream_t s)
     if (int e = encode_map(&tmWs, c.ws, 3, dws, sstr, bs, CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_DATA_TYPE_UINT32))
         return e;
-    const auto kern = conv_mx4_split_kernel<T, NB>;
-    constexpr int kSmem = 1024 + S::kStages * S::kStage + S::kPart + static_cast<int>(sizeof(SplitTail));
-    static_assert(kSmem > 114 * 1024, "two of these kernels would share an SM");
-    static std::atomic<bool> opted[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-        return X1CB_ERR_CUDA;
-    if (!opted[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
-            cudaSuccess)
-            return X1CB_ERR_CUDA;
-        opted[dev].store(true, std::memory_order_release);
-    }
     cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(units * split), 1, 1);
-    cfg.blockDim = dim3(kSplitThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = split;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, tmX, tmW, tmXs, tmWs, a) == cudaSuccess ? X1CB_OK
-                                                                                 : X1CB_ERR_CUDA;
+    Ke::configure(cfg, attr, units, split, s);
+    return cudaLaunchKernelEx(&cfg, conv_mx4_split_kernel<T, NB>, tmX, tmW, tmXs, tmWs, a) ==
+                   cudaSuccess
+               ? X1CB_OK
+               : X1CB_ERR_CUDA;
 }
 
-template <typename T> int run_rows(const Mx4Call &c, int sms, cudaStream_t s)
+template <typename T> int run_rows(const Mx4Call &c, cudaStream_t s)
 {
-    return c.M <= 16   ? run<T, 16>(c, sms, s)
-           : c.M <= 32 ? run<T, 32>(c, sms, s)
-                       : run<T, 64>(c, sms, s);
+    return c.M <= 16 ? run<T, 16>(c, s) : c.M <= 32 ? run<T, 32>(c, s) : run<T, 64>(c, s);
 }
 
 }  // namespace
 
+// More than 64 rows: the split pays where K is long and the chip holds all of the
+// units at once, in us against 128-row tiles: 256 x 2400 x 384 7.2 and 8.8, 100 x 2048 x
+// 512 6.5 and 7.2, 196 x 4096 x 1024 (clusters of four) 8.2 and 9.9; but 100 x 1024 x 256
+// 6.9 and 5.8, 784 x 2400 x 384 (of two) 9.9 and 8.9.
+bool conv_mx4_split_pays(const Mx4Call &c)
+{
+    const int k_steps = (c.K + 255) / 256;
+    const long long units = units_of(c, 64);
+    Fit fit;
+    if (k_steps < 8 || units > 37 || Kernel<float, 64>::prepare(fit) != X1CB_OK)
+        return false;
+    const int split = split_for(units, k_steps, fit);
+    return split == 8 || (split == 4 && k_steps >= 10);
+}
+
 int launch_conv_mx4_split(const Mx4Call &c, cudaStream_t s)
 {
-    int sms = 0;
-    if (int e = current_sms(sms))
-        return e;
-    return c.dtype == X1CB_F32    ? run_rows<float>(c, sms, s)
-           : c.dtype == X1CB_BF16 ? run_rows<__nv_bfloat16>(c, sms, s)
-                                  : run_rows<__half>(c, sms, s);
+    return c.dtype == X1CB_F32    ? run_rows<float>(c, s)
+           : c.dtype == X1CB_BF16 ? run_rows<__nv_bfloat16>(c, s)
+                                  : run_rows<__half>(c, s);
 }
 
 }  // namespace x1cb
