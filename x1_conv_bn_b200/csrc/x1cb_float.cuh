@@ -308,14 +308,26 @@ __device__ __forceinline__ void e2m1_to_half(uint32_t codes, __half2 (&h)[4])
         h[i] = *reinterpret_cast<const __half2 *>(&r[i]);
 }
 
-// Zeroes the scale bytes of rows M .. 128*ceil(M/128) - 1 (threads tid of n).
+// Zeroes the scale bytes of rows M .. 128*ceil(M/128) - 1 (threads tid of n): of
+// each 16 bytes of the last tiles, which hold the rows g, g + 32, g + 64 and g + 96.
 __device__ __forceinline__ void mx4_zero_row_padding(uint8_t *sf, long long M, int kt, int tid,
                                                      int n)
 {
-    const int rows = static_cast<int>((128 - (M & 127)) & 127);
-    for (int i = tid; i < rows * kt; i += n) {
-        const size_t at = mx4_scale_at(M + i / kt, (i % kt) * 4, kt);
-        *reinterpret_cast<uint32_t *>(sf + at) = 0u;
+    const int first = static_cast<int>(M & 127);
+    if (first == 0)
+        return;
+    uint4 *to = reinterpret_cast<uint4 *>(sf + static_cast<size_t>(M >> 7) * kt * 512);
+    for (int i = tid; i < kt * 32; i += n) {
+        const int g = i & 31;
+        if (g >= first) {
+            to[i] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            uint32_t *w = reinterpret_cast<uint32_t *>(to + i);
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                if (g + 32 * q >= first)
+                    w[q] = 0u;
+        }
     }
 }
 
