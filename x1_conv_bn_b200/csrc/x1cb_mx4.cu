@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kBlock)
     const int r0 = c.rows > 1 ? threadIdx.x / c.nv : 0;
     const int step = gridDim.x * c.rows;
     const size_t x_step = static_cast<size_t>(step) * c.K;
-    for (int v0 = 0; v0 < c.nv; v0 += kBlock) {
+    for (int v0 = blockIdx.y * kBlock; v0 < c.nv; v0 += gridDim.y * kBlock) {
         const int v = v0 + threadIdx.x - r0 * c.nv;
         const bool active = r0 < c.rows && v < c.nv;
         const int blk = v / L;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kBlock)
             left = left > kDepth * step ? left - kDepth * step : 0;
         }
     }
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0)
         mx4_zero_row_padding(sf, c.M, kt, threadIdx.x, kBlock);
 }
 
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kBlock)
         return;
     const int step = gridDim.x * c.rows;
     const size_t x_step = static_cast<size_t>(step) * c.K;
-    for (int v = threadIdx.x - r0 * c.nv; v < c.nv; v += kBlock) {
+    for (int v = blockIdx.y * kBlock + threadIdx.x - r0 * c.nv; v < c.nv; v += gridDim.y * kBlock) {
         const int blk = v / 4;
         const uint8_t *scales = sf + static_cast<size_t>(blk >> 2) * 512 + (blk & 3);
         const int first = blockIdx.x * c.rows + r0;
@@ -295,11 +295,14 @@ Cover cover(long long M, int K, int nv)
 // Blocks for kDepth rows a thread, but no more than `deep` per SM.  Writing more
 // than it reads, dequantisation gains from many short blocks (200704 x 512 to
 // bf16: 51.8 us with 8, 45.0 with 32); quantisation does not (45.3 and 49.3).
-int blocks_for(const Cover &c, int deep)
+// Few long rows are cut into pieces besides (quantising 200 x 8192 of float32 7.0 us
+// with whole rows, 3.0 so; 1 x 32768 32.1 and 3.7).
+dim3 blocks_for(const Cover &c, int deep)
 {
-    const int all = (c.M + c.rows - 1) / c.rows;
+    const int all = (c.M + c.rows - 1) / c.rows, pieces = (c.nv + kBlock - 1) / kBlock;
     const int want = (all + kDepth - 1) / kDepth;
-    return std::min(std::max(want, std::min(all, 148)), 148 * deep);
+    const int x = std::min(std::max(want, std::min(all, 148)), 148 * deep);
+    return dim3(x, std::min(pieces, std::max(1, 148 * 8 / x)));
 }
 
 template <typename T> const void *quantize_fn()
@@ -326,7 +329,7 @@ int launch_quantize_mx4(const void *x, int dtype, uint8_t *q, uint8_t *sf, long 
                                          : quantize_fn<__half>();
     Cover c = cover(M, K, K / (dtype == X1CB_F32 ? 4 : 8));
     void *params[] = {&x, &q, &sf, &c};
-    return launch(k, dim3(blocks_for(c, 8)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
+    return launch(k, blocks_for(c, 8), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
 }
 
 int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtype, long long M,
@@ -337,7 +340,7 @@ int launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, void *x, int dtyp
                                          : dequantize_fn<__half>();
     Cover c = cover(M, K, K / 8);
     void *params[] = {&q, &sf, &x, &c};
-    return launch(k, dim3(blocks_for(c, 32)), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
+    return launch(k, blocks_for(c, 32), s, params) == cudaSuccess ? X1CB_OK : X1CB_ERR_CUDA;
 }
 
 // One row: conv_row_kernel.  Up to 64, and a few more where K is long: the weights
