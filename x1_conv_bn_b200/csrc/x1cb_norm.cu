@@ -582,6 +582,8 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
     const int pl = quotient(threadIdx.x, a.div_nv);
     const int per_lane = quotient(px, a.div_lanes), more = px - per_lane * a.lanes;
     const int mine = pl < a.lanes ? per_lane + (pl < more) : 0;
+    // vectors in flight (64 x 224 x 224 x 64 of bfloat16: 276 us with four, 252 with eight)
+    constexpr int kDeep = 2 * kBatch;
     using O = Out<T, V, OUT, true>;  // (results do not push the input out of L2)
     const int most = O::kWhole ? per_lane + (more > 0) : mine;  // of the block
     const size_t step = static_cast<size_t>(a.lanes) * a.C;
@@ -598,21 +600,21 @@ __global__ void __launch_bounds__(kBlock) norm_apply_kernel(NormArgs a)
         const T *x = static_cast<const T *>(a.x) + base;
         const T *r = a.r ? static_cast<const T *>(a.r) + base : nullptr;
         O out(a, b, p0 + (active ? pl : 0), c);
-        for (int i0 = 0; i0 < most; i0 += kBatch) {
-            Vec<T, V> v[kBatch], rv[kBatch];
+        for (int i0 = 0; i0 < most; i0 += kDeep) {
+            Vec<T, V> v[kDeep], rv[kDeep];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
+            for (int j = 0; j < kDeep; ++j) {
                 if (i0 + j < n) {
                     v[j] = load_vec<T, V>(x + j * step);
                     if (r)
                         rv[j] = load_vec<T, V>(r + j * step);
                 }
             }
-            x += kBatch * step;
+            x += kDeep * step;
             if (r)
-                r += kBatch * step;
+                r += kDeep * step;
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
+            for (int j = 0; j < kDeep; ++j) {
                 if (O::kWhole ? i0 + j < most : i0 + j < n) {
                     F2 y[kPairs<V>];
                     f.apply(v[j], r ? &rv[j] : nullptr, y);
