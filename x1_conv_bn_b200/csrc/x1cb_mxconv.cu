@@ -29,10 +29,11 @@
 // has 512 columns, and the scales need theirs: two accumulators of 256 share
 // 128, which are drained first, and the next tile's MMAs start when they are in
 // registers.
-// 16384 x 4096 x 4096 (pair): 121 us, 4.5 PFLOP/s, bound by the tensor pipe while
-// a tile's K loop runs (6 PFLOP/s) and by the hand-over between tiles; in a long run
-// the power cap takes it to 139.  200704 x 128 x 512 with a shortcut (one CTA): 79
-// us, 5.3 TB/s; without one 43 us, 5.1 TB/s: bound by memory.
+// 16384 x 4096 x 4096 (pair): 121 us, 4.5 PFLOP/s.  The K loop runs at 6.1 PFLOP/s, bound
+// by L2 (a stage of 35 KB per SM in 0.40 us is 12.9 TB/s over the chip; the tensor pipe
+// alone would take 0.31), and every tile adds 1.4 us of hand-over; in a long run the
+// power cap takes it to 142.  200704 x 128 x 512 with a shortcut (one CTA): 79 us, 5.4
+// TB/s; without one 44 us, 5.0 TB/s: bound by memory.
 // Every wait is bounded: on a timeout the CTA raises an abort flag, records a
 // status bit, lets its copies and MMAs land and leaves.
 #include <cuda_runtime.h>
@@ -776,7 +777,11 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
     if (tiles > 0x7fffffffLL - sms)
         return X1CB_ERR_SHAPE;
     a.tiles = static_cast<int>(tiles);
-    a.io = kPair ? (a.k_steps >= 12 ? 1 : 2) : c.r && a.k_steps <= 2 ? 2 : 1;
+    // A second box per stream where the epilogue is the longer part, at the cost of
+    // ring stages.  Pair, one box against two: 16384 x 1024 x 4096 55.5 and 49.5, x 2048
+    // 73.8 and 77.0; 50176 x 2048 x 256 with a shortcut 28.7 and 27.9.  One CTA, with a
+    // shortcut: 200704 x 128 x 512 86.7 and 80.0, x 512 91.0 and 95.7.
+    a.io = kPair ? (a.k_steps >= (c.r ? 12 : 8) ? 1 : 2) : c.r && a.k_steps == 1 ? 2 : 1;
     const int epi = ((kIo ? 2 * S::kGroups * a.io * kIoBox : S::kEpiWarps * kPatch) + 1023) & ~1023;
     const int fixed = 1024 + epi + static_cast<int>(sizeof(Tail));
     a.stages = std::min({(232448 - fixed) / S::kStage, S::kSfStages, 8});
@@ -855,10 +860,15 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
 template <typename T> int run_tile(const Mx4Call &c, int sms, cudaStream_t s)
 {
     const bool io = static_cast<size_t>(c.N) * sizeof(T) % 16 == 0;
+    // Tiles of 64 channels against 128: 200000 x 256 x 64 13.3 and 14.8 us.
     if (c.N <= 64)
         return io ? run<T, 64, false, true>(c, sms, s) : run<T, 64, false, false>(c, sms, s);
     const long long pairs = (c.M + 255) / 256 * ((c.N + 255) / 256);
-    if (pairs >= sms / 2 && c.K >= 1024)
+    // Pairs need a K loop that hides their hand-over, and at K = 1024 tiles enough that
+    // the last round counts for little: 128 x 128 against pairs, 16384 x 512 x 4096 38.8
+    // and 42.1 us, x 1024 57.5 and 49.9, x 2048 99.5 and 77.0; 5000 x 1024 x 2048 (160
+    // tiles) 13.8 and 14.7, 9472 x 4096 x 512 (74) 17.7 and 15.6.
+    if (pairs >= (c.K >= 2048 ? sms / 2 : 3 * (sms / 2)) && c.K >= 1024)
         return io ? run<T, 256, true, true>(c, sms, s) : run<T, 256, true, false>(c, sms, s);
     return io ? run<T, 128, false, true>(c, sms, s) : run<T, 128, false, false>(c, sms, s);
 }
