@@ -841,7 +841,7 @@ Plan search_plan(int dtype, int B, int HW, int C, int G, bool whole_blocks, bool
     long long unit = cg;
     while (unit % p.V || (whole_blocks && unit % 32))
         unit += cg;
-    // The two launches, in us: 28.9 MB of input 22.9, 51.4 MB 33.0, 205 MB 123.  The
+    // The two launches, in us: 28.9 MB of input 21.8, 51.4 MB 30.7, 205 MB 123.  The
     // form is chosen without regard to a shortcut, for the workspace's sake.
     const double two = 10. + 0.55e-6 * B * static_cast<double>(HW) * C * elt;
     double best = 1e30, plain = 1e30;
