@@ -449,6 +449,30 @@ def test_calls_on_two_streams_at_once():
         assert torch.equal(a, b)
 
 
+def test_views_off_their_alignment_or_strided():
+    """A contiguous view that starts off 16 bytes and a strided one are refused."""
+    base = torch.randn(2 * 3 * 3 * 64 + 1, device=DEV).bfloat16()
+    off = base[1:].view(2, 3, 3, 64)
+    for call in (lambda v: X.group_norm_act(v, None, None, 4),
+                 lambda v: X.group_norm_act_i8(v, None, None, 4, 1.0),
+                 lambda v: X.group_norm_act_mx4(v, None, None, 4), X.x1cb_quantize_mx4):
+        with pytest.raises(X.X1cbError) as e:
+            call(off)
+        assert e.value.status == X.X1CB_ERR_ALIGN
+        with pytest.raises(ValueError):
+            call(base[:-1].view(2, 3, 64, 3).transpose(2, 3))
+    codes = torch.zeros(4 * 32 + 1, dtype=torch.uint8, device=DEV)
+    sf = torch.zeros(X.mx4_scale_shape(4, 64), dtype=torch.uint8, device=DEV)
+    with pytest.raises(X.X1cbError) as e:
+        X.x1cb_dequantize_mx4(codes[1:].view(4, 32), sf)
+    assert e.value.status == X.X1CB_ERR_ALIGN
+    w, ws = X.x1cb_quantize_mx4(torch.ones(8, 64, device=DEV))
+    with pytest.raises(X.X1cbError) as e:
+        X.conv1x1_bias_add_act_mx4(codes[1:].view(1, 2, 2, 32), sf, w, ws)
+    assert e.value.status == X.X1CB_ERR_ALIGN
+    _clean()
+
+
 # ---- together --------------------------------------------------------------------
 
 @pytest.mark.parametrize("shape", [(2, 14, 14, 256, 32, 64), (1, 1, 1, 2048, 32, 1000),

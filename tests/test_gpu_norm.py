@@ -261,6 +261,23 @@ def test_many_chunks():
         assert torch.equal(got, X.group_norm_act(x, gamma, beta, G, act="none"))
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("shape,G", [((2, 301, 299, 96), 3), ((1, 700, 513, 128), 32),
+                                     ((40, 150, 160, 32), 8)])
+def test_large_images_every_output(shape, G, dtype):
+    """Images that do not fit a cluster, several at a time and in several turns, to
+    each form of output, with a shortcut."""
+    x, gamma, beta, r = _inputs(shape, dtype, 50, res=True)
+    y, size = F.group_norm(x, gamma, beta, G, 1e-5, r, "relu")
+    tol = F.norm_tolerance(y, size)
+    _close(X.group_norm_act(x, gamma, beta, G, r=r), y, F.norm_tolerance(y, size, dtype))
+    q, sf = X.group_norm_act_mx4(x, gamma, beta, G, r=r)
+    _check_mx4(q, sf, y, tol)
+    got = X.x1cb_unpack_act(X.group_norm_act_i8(x, gamma, beta, G, 37.5, r=r))
+    t = (y * 37.5).clamp(-128, 127)
+    _close(got, t, 0.5 + 37.5 * tol + t.abs() * F.U32)
+
+
 def test_more_than_two_to_the_31_elements():
     """Offsets pass 32 bits: the last images come out as they do alone, to a step
     of bfloat16 (another plan may join the statistics in another order)."""
