@@ -520,3 +520,50 @@ def test_norm_feeds_the_int8_convolution(oracle):
     img = X.x1cb_unpack_act(q).cpu()
     ref = oracle.pack_act(oracle.conv(img, inp.w, inp.bias, inp.m, inp.S, None, 0))
     assert torch.equal(got.cpu(), ref)
+
+
+@pytest.mark.parametrize("rows,Ic,Oc", [(1, 2048, 1000), (1, 4096, 2500), (1, 96, 7), (2, 2048, 1000),
+                                        (40, 1024, 130), (300, 544, 200), (300, 96, 50),
+                                        (4864, 2048, 1024)])
+@pytest.mark.parametrize("swap", [False, True])
+def test_conv_opposite_scales(rows, Ic, Oc, swap):
+    """Scales at opposite ends of their range (bytes 1 to 253) whose products are
+    near 1: only the product itself may overflow, whichever side is the large
+    one.  Its sums fit 24 bits in any order, so the result is exact."""
+    g, KB = _gen(rows + Ic), Ic // 32
+    e = torch.tensor([125, -125, 118, -100, 0], device=DEV).repeat(-(-KB // 5))[:KB]
+    if swap:
+        e = -e
+    pair = []
+    for n, sign, spread in ((rows, -1, 1), (Oc, 1, 0)):
+        codes = torch.randint(0, 16, (n, Ic), generator=g, device=DEV)
+        s = 127 + sign * e + torch.randint(-spread, spread + 1, (n, KB), generator=g, device=DEV)
+        pair.append((F.pack_mx4(codes, s), F.values_mx4(codes, s)))
+    (x, xs), xv = pair[0]
+    (w, ws), wv = pair[1]
+    # terms are multiples of 1/8 and at most 36 * 2 = 72: 4096 of them stay below 2^19
+    want = xv @ wv.T
+    for dtype in (torch.float32, torch.bfloat16):
+        got = X.conv1x1_bias_add_act_mx4(x.view(1, rows, 1, Ic // 2), xs, w, ws, act="none", dtype=dtype)
+        _clean()
+        assert torch.equal(got.view(rows, Oc), want.to(dtype))
+
+
+@pytest.mark.parametrize("rows", [1, 2, 70])
+def test_conv_not_a_number_beside_the_smallest_scale(rows):
+    """A block of scale 255 makes its row (or channel) NaN whatever the other
+    side's scale is, the smallest (byte 0) among them."""
+    g = _gen(8)
+    codes, wcodes = (torch.randint(0, 16, (n, 128), generator=g, device=DEV) for n in (rows, 40))
+    s = torch.full((rows, 4), 127, device=DEV)
+    t = torch.full((40, 4), 127, device=DEV)
+    s[rows - 1, 1], t[:, 1] = 255, 0
+    t[3, 2], s[:, 2] = 255, 0
+    (x, xs), (w, ws) = F.pack_mx4(codes, s), F.pack_mx4(wcodes, t)
+    got = X.conv1x1_bias_add_act_mx4(x.view(1, rows, 1, 64), xs, w, ws, act="none",
+                                     dtype=torch.float32).view(rows, 40)
+    _clean()
+    bad = torch.zeros(rows, 40, dtype=torch.bool, device=DEV)
+    bad[rows - 1] = True
+    bad[:, 3] = True
+    assert torch.equal(torch.isnan(got), bad)
