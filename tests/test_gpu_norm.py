@@ -335,3 +335,31 @@ def test_threads_at_once():
     for t in threads:
         t.join()
     assert not wrong
+
+
+OFF_CENTRE = [  # B, H, W, C, G: groups of many values, kept on chip or in two launches
+    (1, 1, 1, 8191, 1),   # a channel to an entry of the join
+    (1, 1, 1, 8192, 1),   # four channels to one
+    (1, 7, 7, 2050, 1),
+    (1, 16, 16, 4, 1),
+    (1, 40, 30, 32, 4),
+    (2, 28, 28, 256, 1),
+    (1, 112, 112, 64, 1),
+    (1, 301, 299, 40, 5),
+    (1, 600, 500, 24, 4),
+]
+
+
+@pytest.mark.parametrize("shape", OFF_CENTRE, ids=[str(s) for s in OFF_CENTRE])
+@pytest.mark.parametrize("where", ["channel", "pixel", "column"])
+@pytest.mark.parametrize("far", [30.0, 100.0, 1000.0])
+def test_first_values_far_off(shape, where, far):
+    """The values that the sums start from lie away from all others: the first
+    channel, the first pixel or the first column of every image."""
+    *s, G = shape
+    g = torch.Generator(device=DEV).manual_seed(11)
+    x = torch.randn(s, generator=g, device=DEV)
+    x[{"channel": (..., 0), "pixel": (slice(None), 0, 0), "column": (slice(None), slice(None), 0)}[where]] += far
+    y, size = F.group_norm(x, None, None, G, 1e-5)
+    got = X.group_norm_act(x, None, None, G, act="none")
+    _close(got, y, F.norm_tolerance(y, size))

@@ -144,20 +144,16 @@ struct Joined {
     double mean, m2;
 };
 
-// Joins the (mean, M2) that a block's threads wrote for one group: entry v of
-// pixel lane l at buf[l * pitch + v], v < width, each standing for n * each
-// values, n = base (+ 1 for the first `more` lanes).  The w lanes that share the
-// group take the pixel lanes in turn, and where those are fewer (many channels) a
-// pixel lane's entries; whole warps call it.
-__device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int base, int more,
-                                               int lanes, int pitch, int width, int each, int w,
-                                               int log_wl, bool active)
-{
-    float s1 = 0.f, s2 = 0.f, ref = 0.f;
-    if (active) {
-        ref = buf[0].x;
-        const int filled = base ? lanes : more;  // lanes with pixels
+// What a group's lanes join (see join_threads).
+struct Entries {
+    const float2 *buf;
+    int filled, base, more, pitch, width, each, w, log_wl;
+
+    // S1 = sum n (mean - at) and S2 = sum M2 + n (mean - at)^2, at = ref + shift.
+    __device__ __forceinline__ float2 sums(float ref, float shift) const
+    {
         const int lane = threadIdx.x & (w - 1), wl = 1 << log_wl, wv = w >> log_wl;
+        float s1 = 0.f, s2 = 0.f;
         for (int l = lane & (wl - 1); l < filled; l += wl) {
             const float n = static_cast<float>((base + (l < more)) * each);
             float t = 0.f, u = 0.f, m = 0.f;
@@ -165,7 +161,7 @@ __device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int ba
 #pragma unroll 2
             for (int v = lane >> log_wl; v < width; v += wv) {
                 const float2 e = p[v];
-                const float d = e.x - ref;
+                const float d = e.x - ref - shift;
                 t += d;
                 u = fmaf(d, d, u);
                 m += e.y;
@@ -173,11 +169,44 @@ __device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int ba
             s1 = fmaf(n, t, s1);
             s2 += fmaf(n, u, m);
         }
+        return make_float2(lanes_sum(s1, w), lanes_sum(s2, w));
     }
-    s1 = lanes_sum(s1, w);
-    s2 = lanes_sum(s2, w);
-    const float off = __fdividef(s1, static_cast<float>(px) * static_cast<float>(width * each));
-    return Joined{static_cast<double>(ref) + off, fmaxf(fmaf(-s1, off, s2), 0.f)};
+};
+// (seldom called: inlined it costs norm_cluster_kernel registers, 256 x 28 x 28 x 512 to
+// MX4 96 us against 90)
+__device__ __noinline__ float2 sums_about(Entries e, float ref, float shift)
+{
+    return e.sums(ref, shift);
+}
+
+// Joins the (mean, M2) that a block's threads wrote for one group: entry v of
+// pixel lane l at buf[l * pitch + v], v < width, each standing for n * each
+// values, n = base (+ 1 for the first `more` lanes).  The w lanes that share the
+// group take the pixel lanes in turn, and where those are fewer (many channels) a
+// pixel lane's entries; whole warps call it.  The sums are taken about the first
+// entry's mean.  Where that lies so far off that S2 - S1^2/n would lose more than
+// four bits (of 8191 entries, the first 1000 spreads away: 1e-3 of the variance), the
+// group goes through them once more about the mean it found.  (Always twice:
+// 256 x 28 x 28 x 512 with a shortcut 119 us, in 64 bits 114, so 110.)
+template <bool kInline>
+__device__ __forceinline__ Joined join_threads(const float2 *buf, int px, int base, int more,
+                                               int lanes, int pitch, int width, int each, int w,
+                                               int log_wl, bool active)
+{
+    const Entries e{buf, !active ? 0 : base ? lanes : more, base, more, pitch, width, each, w, log_wl};
+    const float ref = active ? buf[0].x : 0.f;
+    const float count = static_cast<float>(px) * static_cast<float>(width * each);
+    const float2 s = e.sums(ref, 0.f);
+    const float off = __fdividef(s.x, count), rest = fmaf(-s.x, off, s.y);
+    Joined r{static_cast<double>(ref) + off, fmaxf(rest, 0.f)};
+    const bool again = rest < 0.0625f * s.y;
+    if (__builtin_expect(__any_sync(0xffffffffu, again), 0)) {
+        const float2 t = kInline ? e.sums(ref, off) : sums_about(e, ref, off);
+        const float by = __fdividef(t.x, count);
+        if (again)
+            r = Joined{static_cast<double>(ref) + off + by, fmaxf(fmaf(-t.x, by, t.y), 0.f)};
+    }
+    return r;
 }
 
 // Lanes per group so that a block's threads cover all groups at once where they can.
@@ -308,7 +337,7 @@ template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stat
     const int w = join_width(a.G);
     for (int g0 = 0; g0 < a.G; g0 += kBlock / w) {
         const int g = g0 + threadIdx.x / w;
-        const Joined r = join_threads(buf + g * width, px, per_lane, more, a.lanes, pitch,
+        const Joined r = join_threads<true>(buf + g * width, px, per_lane, more, a.lanes, pitch,
                                       width, each, w, a.log_wl, g < a.G);
         if (g < a.G && threadIdx.x % w == 0)
             a.part[(static_cast<size_t>(b) * a.chunks + blockIdx.x) * a.G + g] =
@@ -713,8 +742,8 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
         const int w = join_width(groups), width = a.cg / each, pitch = a.Cs / each;
         for (int g0 = 0; g0 < groups; g0 += kBlock / w) {
             const int g = g0 + threadIdx.x / w;
-            const Joined t = join_threads(buf + g * width, px, per_lane, more, a.lanes, pitch,
-                                          width, each, w, a.log_wl, g < groups && px > 0);
+            const Joined t = join_threads<false>(buf + g * width, px, per_lane, more, a.lanes, pitch,
+                                                 width, each, w, a.log_wl, g < groups && px > 0);
             if (g < groups && threadIdx.x % w == 0) {
                 if (ctas == 1)
                     coef[g] = make_coef(t, a.inv_count, a.eps);
