@@ -363,3 +363,16 @@ def test_first_values_far_off(shape, where, far):
     y, size = F.group_norm(x, None, None, G, 1e-5)
     got = X.group_norm_act(x, None, None, G, act="none")
     _close(got, y, F.norm_tolerance(y, size))
+
+
+@pytest.mark.parametrize("shape", [(1000, 48, 48, 7, 7), (1, 148, 128, 1031, 1031)])
+@pytest.mark.parametrize("far", [30.0, 1000.0])
+def test_first_of_a_long_run_far_off(shape, far):
+    """One thread's 64 pixels hold an image's only far value, their first."""
+    *s, G = shape
+    g = torch.Generator(device=DEV).manual_seed(12)
+    x = torch.randn(s, generator=g, device=DEV)
+    x[:, 0, 0] += far
+    y, size = F.group_norm(x, None, None, G, 1e-5)
+    got = X.group_norm_act(x, None, None, G, act="none")
+    _close(got, y, F.norm_tolerance(y, size))

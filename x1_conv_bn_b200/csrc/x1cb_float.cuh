@@ -83,6 +83,8 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
     return d;
 }
 
+__device__ __forceinline__ F2 neg2(F2 a) { return a ^ 0x8000000080000000ull; }
+
 // Pairs of a vector of V elements; an odd single element leaves the upper half 0.
 template <int V> constexpr int kPairs = (V + 1) / 2;
 template <typename T, int V>

@@ -2,14 +2,17 @@
 // int8 NC/32HW32 or MX4 output.
 //
 // Statistics: a thread owns V neighbouring channels and walks down up to 64
-// pixels.  Per channel it sums d = x - k and d^2 about the first value k it met,
-// which gives its mean and its sum of squares about the mean, M2 = sum d^2 -
-// (sum d)^2/n.  k being one of the n values, n (mean - k)^2 <= n M2, so the
-// subtraction costs at most a factor n of the relative rounding error, however
-// far the data lies from zero.  A block joins its threads' (n, mean, M2) about
-// the mean R of one of them, S1 = sum n (mean - R) and S2 = sum M2 + n (mean -
-// R)^2, by the same argument with the number of threads; parts of different
-// blocks are joined in 64 bits.  All in a fixed order.
+// pixels.  Per channel it sums d = x - k and d^2 about a value k, which gives its
+// mean and its sum of squares about the mean, M2 = sum d^2 - (sum d)^2/n.  k is the
+// first value and, behind the first eighth of the pixels, the mean of those
+// (norm_stats_kernel: behind the 8th and the 32nd).  k being the mean of m of the n
+// values, n (mean - k)^2 <= (n/m) M2, so the subtraction costs at most a factor 8 of
+// the relative rounding error, however far the data lies from zero or one value from
+// the others (about the first alone, with that one of 64 pixels far off, the results
+// were 8 times their tolerance away).  A block joins its threads' (n, mean, M2) about the mean R of one of
+// them, S1 = sum n (mean - R) and S2 = sum M2 + n (mean - R)^2, and where R lies so
+// far off that S2 - S1^2/n would lose more than four bits, once more about the mean
+// found; parts of different blocks are joined in 64 bits.  All in a fixed order.
 //
 // Two forms.  Where an image (or a slice of its channels that holds whole
 // groups) fits the shared memory of a cluster of up to eight CTAs, one launch
@@ -19,8 +22,8 @@
 // the normalisation, over as many images at a time as stay in L2 between them (and
 // one between the two that joins the chunks, where there are many).
 //
-// 256 x 28 x 28 x 512 of bfloat16 with a shortcut: 111 us, 5.6 TB/s, bound by memory
-// (without one 74 us, 5.6 TB/s); to int8 (128 images) 40 us and to MX4 92 us, bound by
+// 256 x 28 x 28 x 512 of bfloat16 with a shortcut: 112 us, 5.5 TB/s, bound by memory
+// (without one 74 us, 5.6 TB/s); to int8 (128 images) 41 us and to MX4 92 us, bound by
 // instructions: two CTAs fit an SM, and while they round, nothing loads.  SiLU adds
 // 26 us of exponentials and divisions.  Two launches: 1 x 2048 x 2048 x 256 1130 us, x
 // read twice and y written at 5.7 TB/s.  1 x 7 x 7 x 2048: 3.8 us, latency.
@@ -99,6 +102,20 @@ template <int V> struct Sums {
             const F2 d = add2(f[i], k[i]);
             s[i] = add2(s[i], d);
             q[i] = fma2(d, d, q[i]);
+        }
+    }
+    // Moves k to the mean of the n values so far: by d to k', sum (x - k') = s - n d
+    // and sum (x - k')^2 = q - d (s + (s - n d)).
+    __device__ __forceinline__ void move(float n, float inv)
+    {
+#pragma unroll
+        for (int i = 0; i < kPairs<V>; ++i) {
+            const F2 m = fma2(s[i], f2(-inv, -inv), k[i]);  // -k'
+            const F2 d = add2(m, neg2(k[i]));              // -d, as m was rounded
+            const F2 t = fma2(d, f2(n, n), s[i]);
+            q[i] = fma2(d, add2(s[i], t), q[i]);
+            s[i] = t;
+            k[i] = m;
         }
     }
     // Writes (mean, M2) of each channel, or of all V together (one), to out.
@@ -329,6 +346,8 @@ template <typename T, int V> __global__ void __launch_bounds__(kBlock) norm_stat
                 for (int j = 0; j < kDeep; ++j)
                     if (i0 + j < mine)
                         st.add(v[j]);
+                if ((i0 == 0 || i0 == 24) && mine > i0 + kDeep)
+                    st.move(i0 + kDeep, i0 ? 1.f / 32 : 1.f / 8);
             }
             st.write(mine, one, buf + (pl * a.nv + cv) * (V / each));
         }
@@ -693,14 +712,15 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
         mx4_zero_row_padding(a.sf, static_cast<long long>(a.B) * a.HW, (a.C + 127) / 128,
                              threadIdx.x, kBlock);
     // Every copy of the thread is in flight before the first is used: x in two
-    // groups, so that the sums run behind the arrivals, then the shortcut.
-    const int half = (mine + 1) / 2;
+    // groups, the pixels before k moves and those behind, then the shortcut.  (k moved
+    // behind the 4th and the 16th pixel instead: 117 us for 112 with a shortcut.)
+    const int first = (mine + 7) / 8;
     {
         const T *x = static_cast<const T *>(a.x) + base;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int end = h ? mine : half;
-            for (int i = h ? half : 0; i < end; ++i, x += step) {
+            const int end = h ? mine : first;
+            for (int i = h ? first : 0; i < end; ++i, x += step) {
                 if constexpr (sizeof(Slot) >= 4)
                     copy_async<sizeof(Slot)>(slots + i * kBlock, x);
                 else
@@ -724,12 +744,14 @@ __global__ void __launch_bounds__(kBlock, 3) norm_cluster_kernel(NormArgs a)
         copy_wait<2>();
         if (mine > 0) {
             st.start(slots[0]);
-            for (int i = 1; i < half; ++i)
+            for (int i = 1; i < first; ++i)
                 st.add(slots[i * kBlock]);
+            if (first > 1)
+                st.move(first, __fdividef(1.f, first));
         }
         copy_wait<1>();
         if (mine > 0) {
-            for (int i = half; i < mine; ++i)
+            for (int i = first; i < mine; ++i)
                 st.add(slots[i * kBlock]);
             st.write(mine, one, buf + threadIdx.x * per);
         }
