@@ -168,3 +168,40 @@ def test_marshalling_module_leaves_the_unusual_alone():
     assert f.dequantize(q, s, "bf16") is None
     assert f.conv1x1(q, s, q, s, None, None, 1, 1) is None
     assert f.conv1x1(q, s, q, s, None, None, -1, 7) is None
+
+
+_CHILD = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import x1_conv_bn_b200 as X
+f = X._compiled()
+assert f.raises(16) is None and f.raises(torch.zeros(3)) is None
+try:
+    f.raises(1 << 62)  # no allocator has this
+except (RuntimeError, MemoryError) as e:
+    print("allocation:", type(e).__name__)
+def inside(t):
+    try:
+        f.raises(t)  # a vmap's tensors have no storage of their own
+    except RuntimeError as e:
+        print("address:", type(e).__name__)
+    return t
+torch.vmap(inside)(torch.zeros(2, 3))
+"""
+
+
+def test_marshalling_module_raises():
+    """A C++ exception in the compiled marshalling arrives as a Python one."""
+    import os
+    import subprocess
+    import sys
+
+    from x1_conv_bn_b200 import _build
+
+    _build.build()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _CHILD.format(root=root)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr)
+    assert r.stdout.split("\n")[:2] == ["allocation: RuntimeError", "address: RuntimeError"], r.stdout

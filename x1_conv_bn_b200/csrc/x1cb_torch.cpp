@@ -3,14 +3,16 @@
 // checks and conversions of such a call take twice as long as the library's own
 // part of it (allocation, argument checks, launch).  Every function returns None
 // when anything is out of the ordinary -- an operand that is missing, on another
-// device, strided, of another type or size, or a call that the library refuses --
-// and the binding then takes its own way, which names what is wrong.
+// device, strided, without storage, of another type or size, or a call that the
+// library refuses -- and the binding then takes its own way, which names what is
+// wrong.  C++ exceptions (no memory for a result) leave as their Python ones.
 #include <Python.h>
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -31,10 +33,16 @@ const at::Tensor *operand(PyObject *o, bool &ok, bool optional = false)
     return &THPVariable_Unpack(o);
 }
 
+// A CUDA tensor with sizes, strides and memory of its own (not sparse, nested or
+// the handle of a function transform).
+bool on_gpu(const at::Tensor *t)
+{
+    return t->is_cuda() && t->layout() == at::kStrided && !t->is_nested() && t->has_storage();
+}
+
 bool plain(const at::Tensor *t, at::ScalarType type, int device)
 {
-    return t->is_cuda() && t->get_device() == device && t->scalar_type() == type &&
-           t->is_contiguous() && t->layout() == at::kStrided;
+    return on_gpu(t) && t->get_device() == device && t->scalar_type() == type && t->is_contiguous();
 }
 
 int dtype_code(at::ScalarType t)
@@ -82,7 +90,7 @@ at::Tensor scales_for(int64_t M, int64_t K, const at::TensorOptions &u8)
 }
 
 // norm(kind, x, gamma, beta, G, eps, r, act, q_mul), kind 0 same type, 1 int8, 2 MX4
-PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n)
+PyObject *norm(PyObject *const *args, Py_ssize_t n)
 {
     if (n != 9)
         return none();
@@ -95,7 +103,7 @@ PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n)
     bool ok = G > 0 && G <= INT_MAX;
     const at::Tensor *x = operand(args[1], ok), *gamma = operand(args[2], ok, true);
     const at::Tensor *beta = operand(args[3], ok, true), *r = operand(args[6], ok, true);
-    if (!ok || x->dim() != 4 || !x->is_cuda())
+    if (!ok || !on_gpu(x) || x->dim() != 4)
         return none();
     const int dev = x->get_device(), dt = dtype_code(x->scalar_type());
     const auto s = x->sizes();
@@ -141,11 +149,11 @@ PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n)
 }
 
 // quantize(x)
-PyObject *quantize(PyObject *, PyObject *const *args, Py_ssize_t n)
+PyObject *quantize(PyObject *const *args, Py_ssize_t n)
 {
     bool ok = n == 1;
     const at::Tensor *x = ok ? operand(args[0], ok) : nullptr;
-    if (!ok || x->dim() < 1 || !x->is_cuda())
+    if (!ok || !on_gpu(x) || x->dim() < 1)
         return none();
     const int dev = x->get_device(), dt = dtype_code(x->scalar_type());
     const int64_t K = x->size(-1);
@@ -179,7 +187,7 @@ bool scales_are(const at::Tensor *t, int64_t M, int64_t K)
 }
 
 // dequantize(codes, scales, dtype code)
-PyObject *dequantize(PyObject *, PyObject *const *args, Py_ssize_t n)
+PyObject *dequantize(PyObject *const *args, Py_ssize_t n)
 {
     bool ok = n == 3;
     const long dt = ok ? PyLong_AsLong(args[2]) : -1;
@@ -189,7 +197,7 @@ PyObject *dequantize(PyObject *, PyObject *const *args, Py_ssize_t n)
     }
     at::ScalarType type;
     const at::Tensor *q = ok ? operand(args[0], ok) : nullptr, *sf = ok ? operand(args[1], ok) : nullptr;
-    if (!ok || !dtype_of(dt, type) || q->dim() < 1 || !q->is_cuda())
+    if (!ok || !dtype_of(dt, type) || !on_gpu(q) || q->dim() < 1)
         return none();
     const int dev = q->get_device();
     const int64_t K = 2 * q->size(-1);
@@ -213,7 +221,7 @@ PyObject *dequantize(PyObject *, PyObject *const *args, Py_ssize_t n)
 }
 
 // conv1x1(x, xs, w, ws, bias, r, act, dtype code)
-PyObject *conv1x1(PyObject *, PyObject *const *args, Py_ssize_t n)
+PyObject *conv1x1(PyObject *const *args, Py_ssize_t n)
 {
     bool ok = n == 8;
     const long act = ok ? PyLong_AsLong(args[6]) : -1, dt = ok ? PyLong_AsLong(args[7]) : -1;
@@ -227,7 +235,7 @@ PyObject *conv1x1(PyObject *, PyObject *const *args, Py_ssize_t n)
     const at::Tensor *x = operand(args[0], ok), *xs = operand(args[1], ok), *w = operand(args[2], ok);
     const at::Tensor *ws = operand(args[3], ok), *bias = operand(args[4], ok, true);
     const at::Tensor *r = operand(args[5], ok, true);
-    if (!ok || x->dim() != 4 || w->dim() != 2 || !x->is_cuda())
+    if (!ok || !on_gpu(x) || !on_gpu(w) || x->dim() != 4 || w->dim() != 2)
         return none();
     const int dev = x->get_device();
     if (dev != c10::cuda::current_device() || !plain(x, at::kByte, dev) || !plain(xs, at::kByte, dev) ||
@@ -254,12 +262,41 @@ PyObject *conv1x1(PyObject *, PyObject *const *args, Py_ssize_t n)
     return THPVariable_Wrap(out);
 }
 
-PyMethodDef methods[] = {
-    {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(norm)), METH_FASTCALL, nullptr},
-    {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(quantize)), METH_FASTCALL, nullptr},
-    {"dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(dequantize)), METH_FASTCALL, nullptr},
-    {"conv1x1", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(conv1x1)), METH_FASTCALL, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+// raises(what), for tests: an allocation of `what` bytes of host memory, or the
+// address of tensor `what`.
+PyObject *raises(PyObject *const *args, Py_ssize_t n)
+{
+    if (n == 1 && THPVariable_CheckExact(args[0])) {
+        THPVariable_Unpack(args[0]).data_ptr();
+    } else if (n == 1) {
+        const long long bytes = PyLong_AsLongLong(args[0]);
+        if (PyErr_Occurred())
+            return nullptr;
+        at::empty({bytes}, at::TensorOptions().dtype(at::kByte));
+    }
+    return none();
+}
+
+// What Python calls: F, with its exceptions turned into Python's.
+template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
+PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    return F(args, n);
+    END_HANDLE_TH_ERRORS
+}
+template <PyObject *(*F)(PyObject *const *, Py_ssize_t)> PyMethodDef method(const char *name)
+{
+    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(entry<F>)), METH_FASTCALL,
+            nullptr};
+}
+
+PyMethodDef methods[] = {method<norm>("norm"),
+                         method<quantize>("quantize"),
+                         method<dequantize>("dequantize"),
+                         method<conv1x1>("conv1x1"),
+                         method<raises>("raises"),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_x1cb_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
