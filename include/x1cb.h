@@ -296,7 +296,8 @@ int x1cb_pack_stem_weight(const int8_t *oihw, int8_t *blocked, int Oc, int Cin, 
  * act one of X1CB_ACT_NONE (v), X1CB_ACT_RELU (max(v, 0); NaN stays NaN),
  * X1CB_ACT_SILU (v / (1 + exp(-v))); other values return X1CB_ERR_SHAPE.
  * Sums, statistics and everything between the load and the store are 32-bit;
- * a result is rounded once, to nearest even.  Empty tensors are a no-op.
+ * a result is rounded once, to nearest even.  Empty tensors are a no-op.  All
+ * are forward only (the Python binding refuses operands that require grad).
  * The rules on memory, alignment, overlap, streams and errors above hold
  * (gamma, beta and bias: 4-byte alignment).
  *

@@ -205,3 +205,26 @@ def test_marshalling_module_raises():
                        timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr)
     assert r.stdout.split("\n")[:2] == ["allocation: RuntimeError", "address: RuntimeError"], r.stdout
+
+
+def test_binding_refuses_gradients():
+    """No call has a backward pass: what autograd would have to record is refused
+    by name, and runs (here as far as the check for a GPU) without grad mode."""
+    x, q = torch.zeros(1, 2, 2, 32), torch.zeros(1, 2, 2, 16, dtype=torch.uint8)
+    s, v = torch.zeros(1, 1, 32, 16, dtype=torch.uint8), torch.zeros(32)
+    p = lambda t: torch.nn.Parameter(t.clone())  # noqa: E731
+    norms = (X.group_norm_act, lambda *a, **k: X.group_norm_act_i8(*a, 1.0, **k), X.group_norm_act_mx4)
+    calls = [("x", lambda: X.x1cb_quantize_mx4(p(x))),
+             ("out", lambda: X.x1cb_dequantize_mx4(q, s, dtype=torch.float32, out=p(x))),
+             ("bias", lambda: X.conv1x1_bias_add_act_mx4(q, s, q[0, 0], s, p(v[:2]))),
+             ("r", lambda: X.conv1x1_bias_add_act_mx4(q, s, q[0, 0], s, None, p(x))),
+             ("out", lambda: X.group_norm_act(x, None, None, 4, out=p(x)))]
+    for n in norms:
+        calls += [("x", lambda n=n: n(p(x), None, None, 4)), ("gamma", lambda n=n: n(x, p(v), None, 4)),
+                  ("beta", lambda n=n: n(x, None, p(v), 4)), ("r", lambda n=n: n(x, None, None, 4, r=p(x)))]
+    for name, call in calls:
+        with pytest.raises(ValueError, match=f"^{name} requires grad"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError) as e:
+            call()
+        assert "requires grad" not in str(e.value)

@@ -95,3 +95,31 @@ for t in (x[0].to_sparse(), torch.nested.nested_tensor([x[0, 0], x[1, 0]])):
         raise SystemExit("no error")
 torch.cuda.synchronize()
 """)
+
+
+def test_gradients_are_refused():
+    """An operand that requires grad is refused while grad mode is on, and served
+    without it with the same results."""
+    import x1_conv_bn_b200 as X
+
+    p = lambda t: torch.nn.Parameter(t.clone())  # noqa: E731
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(2, 5, 5, 64, generator=g, device="cuda")
+    v = torch.randn(64, generator=g, device="cuda")
+    q, sf = X.x1cb_quantize_mx4(x)
+    w, ws = X.x1cb_quantize_mx4(torch.randn(64, 64, generator=g, device="cuda"))
+    conv = lambda b, r: X.conv1x1_bias_add_act_mx4(q, sf, w, ws, b, r, dtype=torch.float32)  # noqa: E731
+    cases = [(lambda a: X.group_norm_act(a, v, v, 8), x), (lambda a: X.group_norm_act(x, a, v, 8), v),
+             (lambda a: X.group_norm_act(x, v, a, 8), v), (lambda a: X.group_norm_act(x, v, v, 8, r=a), x),
+             (lambda a: X.group_norm_act_i8(a, v, v, 8, 30.0), x),
+             (lambda a: X.group_norm_act_mx4(x, a, v, 8)[0], v), (lambda a: X.x1cb_quantize_mx4(a)[1], x),
+             (lambda a: conv(a, None), v), (lambda a: conv(None, a), x)]
+    for f, t in cases:
+        want = f(t)
+        with pytest.raises(ValueError, match="requires grad"):
+            f(p(t))
+        for off in (torch.no_grad, torch.inference_mode):
+            with off():
+                got = f(p(t))
+                assert not got.requires_grad and torch.equal(got, want)
+        assert torch.equal(f(p(t).detach()), want)

@@ -441,7 +441,8 @@ def x1cb_pack_weight(oihw, out=None, stream=None):
 # Calls in their ordinary form (operands on the current device, results new, on
 # the current stream) are marshalled by the compiled module _x1cb_torch, which
 # answers None to anything else; the Python below takes that, and names what is
-# wrong.
+# wrong.  All of them are forward only: operands that require grad are refused while
+# grad mode is on.
 _fast = None
 
 
@@ -469,6 +470,15 @@ def _act(act: str) -> int:
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
     return ACTS[act]
+
+
+def _forward_only(**operands):
+    """Refuses a call that autograd would have to record: there is no backward pass."""
+    if torch.is_grad_enabled():
+        for name, t in operands.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} requires grad, and this call has no backward pass: "
+                                 "detach it or call under torch.no_grad()")
 
 
 def _sized(t: Optional[torch.Tensor], shape, name: str):
@@ -580,6 +590,7 @@ def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str =
         y = (_fast or _compiled()).norm(0, x, gamma, beta, G, eps, r, ACTS.get(act, -1), 0.0)
         if y is not None:
             return y
+    _forward_only(x=x, gamma=gamma, beta=beta, r=r, out=out)
     index, shape = _norm_input(x)
     if out is None:
         out = _empty(shape, x.dtype, index, stream)
@@ -598,6 +609,7 @@ def group_norm_act_i8(x, gamma, beta, G: int, q_mul: float, eps: float = 1e-5, r
         y = (_fast or _compiled()).norm(1, x, gamma, beta, G, eps, r, ACTS.get(act, -1), q_mul)
         if y is not None:
             return y
+    _forward_only(x=x, gamma=gamma, beta=beta, r=r)
     index, (B, H, W, C) = _norm_input(x)
     shape = (B, C // 32, H, W, 32)
     if out is None:
@@ -632,6 +644,7 @@ def group_norm_act_mx4(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: s
         y = (_fast or _compiled()).norm(2, x, gamma, beta, G, eps, r, ACTS.get(act, -1), 0.0)
         if y is not None:
             return y
+    _forward_only(x=x, gamma=gamma, beta=beta, r=r)
     index, (B, H, W, C) = _norm_input(x)
     q, sf = _mx4_outs((B, H, W), B * H * W, C, out, index, stream)
     _norm(lib().group_norm_act_mx4, "group_norm_act_mx4", x, gamma, beta, int(G), eps, r, act,
@@ -652,6 +665,7 @@ def x1cb_quantize_mx4(x, out=None, stream=None):
         y = (_fast or _compiled()).quantize(x)
         if y is not None:
             return y
+    _forward_only(x=x)
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be [..., K]")
     *lead, K = x.shape
@@ -669,6 +683,7 @@ def x1cb_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None, stream=None):
         y = (_fast or _compiled()).dequantize(q, sf, DTYPES.get(dtype, -1))
         if y is not None:
             return y
+    _forward_only(out=out)
     if not isinstance(q, torch.Tensor) or q.dim() < 1:
         raise ValueError("codes must be [..., K/2]")
     *lead, half = q.shape
@@ -697,6 +712,7 @@ def conv1x1_bias_add_act_mx4(x, xs, w, ws, bias=None, r=None, act: str = "relu",
                                            DTYPES.get(dtype, -1))
         if y is not None:
             return y
+    _forward_only(bias=bias, r=r, out=out)
     if not isinstance(x, torch.Tensor) or x.dim() != 4:
         raise ValueError("x must be [B, H, W, Ic/2]")
     if not isinstance(w, torch.Tensor) or w.dim() != 2:

@@ -3,13 +3,14 @@
 // checks and conversions of such a call take twice as long as the library's own
 // part of it (allocation, argument checks, launch).  Every function returns None
 // when anything is out of the ordinary -- an operand that is missing, on another
-// device, strided, without storage, of another type or size, or a call that the
-// library refuses -- and the binding then takes its own way, which names what is
+// device, strided, without storage, of another type or size, one that requires
+// grad, or a call that the library refuses -- and the binding then takes its own way, which names what is
 // wrong.  C++ exceptions (no memory for a result) leave as their Python ones.
 #include <Python.h>
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -40,9 +41,10 @@ bool on_gpu(const at::Tensor *t)
     return t->is_cuda() && t->layout() == at::kStrided && !t->is_nested() && t->has_storage();
 }
 
+// (the calls have no backward pass: one that autograd would record is refused)
 bool plain(const at::Tensor *t, at::ScalarType type, int device)
 {
-    return on_gpu(t) && t->get_device() == device && t->scalar_type() == type && t->is_contiguous();
+    return on_gpu(t) && !(t->requires_grad() && at::GradMode::is_enabled()) && t->get_device() == device && t->scalar_type() == type && t->is_contiguous();
 }
 
 int dtype_code(at::ScalarType t)
