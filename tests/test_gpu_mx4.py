@@ -567,3 +567,33 @@ def test_conv_not_a_number_beside_the_smallest_scale(rows):
     bad[rows - 1] = True
     bad[:, 3] = True
     assert torch.equal(torch.isnan(got), bad)
+
+
+@pytest.mark.parametrize("shape,res", [((1, 4, 4, 1024, 256), True), ((2, 6, 5, 512, 512), False),  # K split
+                                       ((40, 16, 16, 2048, 1024), False), ((40, 16, 16, 2048, 1024), True),  # pairs
+                                       ((40, 16, 16, 2048, 1001), True)])
+@pytest.mark.parametrize("limit_ms", [20, 300])
+def test_conv_bounded_wait_of_clusters(shape, res, limit_ms):
+    """A wait that runs out in a CTA of a cluster: the others are told or come to
+    their own end, every copy lands before any of them leaves, and the next call
+    works.  (With 300 ms a CTA's other waits last longer than its exit once did.)"""
+    B, H, W, Ic, Oc = shape
+    g = _gen(14)
+    (x, xs), _ = _operand(B * H * W, Ic, g)
+    (w, ws), _ = _operand(Oc, Ic, g)
+    x = x.view(B, H, W, Ic // 2)
+    r = torch.randn(B, H, W, Oc, generator=g, device=DEV).to(torch.bfloat16) if res else None
+    want = X.conv1x1_bias_add_act_mx4(x, xs, w, ws, None, r)
+    _clean()
+    try:
+        X.x1cb_set_wait_limit_ns(limit_ms * 1_000_000)
+        X.x1cb_debug_inject(1)
+        X.conv1x1_bias_add_act_mx4(x, xs, w, ws, None, r)
+        st, bits = X.x1cb_last_device_error(clear=True)
+    finally:
+        X.x1cb_debug_inject(0)
+        X.x1cb_set_wait_limit_ns(0)
+    assert st == X.X1CB_ERR_TIMEOUT and bits == 2  # the planted wait, and none besides
+    got = X.conv1x1_bias_add_act_mx4(x, xs, w, ws, None, r)
+    _clean()
+    assert torch.equal(got, want)

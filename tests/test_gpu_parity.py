@@ -625,3 +625,26 @@ def test_operands_must_be_memory_of_the_current_device():
     torch.cuda.synchronize()
     with pytest.raises(ValueError):
         X.conv1x1_bn_add_relu_i8(x, w.cpu(), b, m, 0, 24)
+
+
+@pytest.mark.parametrize("limit_ms", [50, 300])
+def test_bounded_wait_of_a_pair(oracle, limit_ms):
+    """The same in a CTA pair: the other CTA is told, no copy of it is in flight
+    when either leaves, and the next call is exact."""
+    s = synth.ConvShape(41, 7, 7, 512, 2048, R=1, has_res=True)
+    assert "cta_pair=1" in X.x1cb_describe_plan(41, 7, 7, 512, 2048, 1, True)
+    inp = synth.conv_inputs(s, 45)
+    want = _gpu_conv(inp)
+    x, w, r = X.x1cb_pack_act(inp.x.to(DEV)), X.x1cb_pack_weight(inp.w.to(DEV)), X.x1cb_pack_act(inp.r.to(DEV))
+    bias, m = inp.bias.to(DEV), inp.m.to(DEV)
+    torch.cuda.synchronize()
+    try:
+        X.x1cb_set_wait_limit_ns(limit_ms * 1_000_000)
+        X.x1cb_debug_inject(1)
+        X.conv1x1_bn_add_relu_i8(x, w, bias, m, inp.m_r, inp.S, r)
+        st, bits = X.x1cb_last_device_error(clear=True)
+    finally:
+        X.x1cb_debug_inject(0)
+        X.x1cb_set_wait_limit_ns(0)
+    assert st == X.X1CB_ERR_TIMEOUT and bits == 2
+    assert torch.equal(_gpu_conv(inp), want)

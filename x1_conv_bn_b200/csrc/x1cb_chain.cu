@@ -958,11 +958,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (threadIdx.x == 0)
         X1CB_TRACE_AT(p.trace, 15, 1);
-    if (threadIdx.x == 0) {
-        mbar_arrive_cluster(mapa_shared(bars.exit_bar(), rank ^ 1u));
-        if (!mbar_drain(bars.exit_bar(), 0, 2 * p.wait_limit_ns + drain_ns))
-            atomicOr(dev_status, kDevDrainFailed);
-    }
+    if (threadIdx.x == 0 && !leave_pair(bars.exit_bar(), rank, ctl, drain_ns))
+        atomicOr(dev_status, kDevDrainFailed);
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();

@@ -727,13 +727,8 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (kPair) {
-        // neither CTA of a pair leaves while the other may still reach it (its
-        // copies complete on rank 0's barriers, its arrivals cross over)
-        if (threadIdx.x == 0) {
-            mbar_arrive_cluster(mapa_shared(exit_bar, rank ^ 1u));
-            if (!mbar_drain(exit_bar, 0, 2 * a.wait_ns + kDrainNs))
-                atomicOr(a.status, kDevDrainFailed);
-        }
+        if (threadIdx.x == 0 && !leave_pair(exit_bar, rank, ctl, kDrainNs))
+            atomicOr(a.status, kDevDrainFailed);
         __syncthreads();
     }
     if (warp == 1) {

@@ -606,6 +606,28 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
                  : "memory");
 }
 
+// Tear-down of a CTA pair, by one thread of each CTA behind its last __syncthreads:
+// neither leaves while the other may still reach it (rank 1's copies complete on
+// rank 0's barriers, arrivals cross over).  A CTA that gave up tells the other, which
+// then leaves its own waits too, and stays a little longer than a copy takes: what
+// rank 1 issued after rank 0 gave up is waited for by nobody else.  The other may have
+// begun its last wait just before it is told, and then drains up to 64 copies and
+// MMAs one by one, each for drain_ns at most; leaving before it has would let its
+// arrivals reach a CTA that is gone.  False: it did not come.
+__device__ __forceinline__ bool leave_pair(uint32_t exit_bar, uint32_t rank, const WaitCtl &ctl,
+                                           uint64_t drain_ns)
+{
+    if (*ctl.abort_flag) {
+        const uint32_t flag = smem_u32(const_cast<const int *>(ctl.abort_flag));
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(flag, rank ^ 1u)), "r"(1)
+                     : "memory");
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 5000000ull;)
+            __nanosleep(10000);
+    }
+    mbar_arrive_cluster(mapa_shared(exit_bar, rank ^ 1u));
+    return mbar_drain(exit_bar, 0, 2 * ctl.limit_ns + 64 * drain_ns);
+}
+
 // Both CTAs of the cluster: every thread arrives and waits (hardware barrier;
 // used once after set-up, when both CTAs are known to be running).
 __device__ __forceinline__ void cluster_sync_all()
