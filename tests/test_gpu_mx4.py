@@ -597,3 +597,29 @@ def test_conv_bounded_wait_of_clusters(shape, res, limit_ms):
     got = X.conv1x1_bias_add_act_mx4(x, xs, w, ws, None, r)
     _clean()
     assert torch.equal(got, want)
+
+
+def test_clusters_on_several_streams():
+    """Pairs with the plain epilogue, pairs with TMA boxes and split clusters at
+    once on streams of their own, again and again: none keeps TMEM or an SM that
+    another waits for with its own, and the results are those of calls alone."""
+    calls = []
+    for k, (B, H, W, Ic, Oc, res) in enumerate([(40, 16, 16, 2048, 1001, True), (40, 16, 16, 2048, 1001, True),
+                                                (40, 16, 16, 2048, 1024, True), (2, 6, 5, 2048, 1500, False)]):
+        g = _gen(20 + k)
+        (x, xs), _ = _operand(B * H * W, Ic, g)
+        (w, ws), _ = _operand(Oc, Ic, g)
+        r = torch.randn(B, H, W, Oc, generator=g, device=DEV).to(torch.bfloat16) if res else None
+        x = x.view(B, H, W, Ic // 2)
+        calls.append(lambda x=x, xs=xs, w=w, ws=ws, r=r, **kw: X.conv1x1_bias_add_act_mx4(x, xs, w, ws, None, r, **kw))
+    want = [c() for c in calls]
+    _clean()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = [[torch.empty_like(y) for _ in range(20)] for y in want]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, s, o in zip(calls, streams, outs):
+            c(out=o[i], stream=s)
+    _clean()
+    for y, o in zip(want, outs):
+        assert all(torch.equal(t, y) for t in o)

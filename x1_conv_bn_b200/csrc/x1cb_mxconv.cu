@@ -747,6 +747,49 @@ CUtensorMapDataType map_type(int dtype)
                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
+// Shared memory of a launch: boxes per stream, ring stages, bytes.
+struct Memory {
+    int io, stages, bytes;
+};
+template <typename S, bool kIo> constexpr Memory memory(bool r, int k_steps)
+{
+    constexpr bool kPair = S::kGroups == 1;
+    Memory m{};
+    // A second box per stream where the epilogue is the longer part, at the cost of
+    // ring stages.  Pair, one box against two: 16384 x 1024 x 4096 55.5 and 49.5, x 2048
+    // 73.8 and 77.0; 50176 x 2048 x 256 with a shortcut 28.7 and 27.9.  One CTA, with a
+    // shortcut: 200704 x 128 x 512 86.7 and 80.0, x 512 91.0 and 95.7.
+    m.io = kPair ? (k_steps >= (r ? 12 : 8) ? 1 : 2) : r && k_steps == 1 ? 2 : 1;
+    const int epi = ((kIo ? 2 * S::kGroups * m.io * kIoBox : S::kEpiWarps * kPatch) + 1023) & ~1023;
+    const int fixed = 1024 + epi + static_cast<int>(sizeof(Tail));
+    m.stages = std::min({(kSmemLimit - fixed) / S::kStage, S::kSfStages, 8});
+    // The plain epilogue's loads need L1: 200000 x 64 x 250 with a shortcut 66.0 us
+    // with all of the shared memory taken by the ring, 61.5 with half of it.
+    if (!kIo && r)
+        m.stages = std::min(m.stages, std::max(2, (110 * 1024 - fixed) / S::kStage));
+    m.bytes = std::max(fixed + m.stages * S::kStage, kSmemAlone);
+    return m;
+}
+
+// Every launch keeps its SM to itself, whatever its registers: clusters that wait
+// for one another's TMEM columns could never end (tcgen05.alloc has no limit).
+template <typename S, bool kIo> constexpr bool alone()
+{
+    for (int k = 1; k <= 16; ++k)
+        for (int r = 0; r < 2; ++r) {
+            const Memory m = memory<S, kIo>(r != 0, k);
+            if (m.bytes < kSmemAlone || m.bytes > kSmemLimit || m.stages < 2)
+                return false;
+        }
+    return true;
+}
+template <int BN, bool kPair> constexpr bool both_alone()
+{
+    return alone<Shape<BN, kPair>, true>() && alone<Shape<BN, kPair>, false>();
+}
+static_assert(both_alone<64, false>() && both_alone<128, false>() && both_alone<256, true>(),
+              "a kernel that holds TMEM would share its SM");
+
 template <typename T, int BN, bool kPair, bool kIo>
 int run(const Mx4Call &c, int sms, cudaStream_t s)
 {
@@ -772,19 +815,9 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
     if (tiles > 0x7fffffffLL - sms)
         return X1CB_ERR_SHAPE;
     a.tiles = static_cast<int>(tiles);
-    // A second box per stream where the epilogue is the longer part, at the cost of
-    // ring stages.  Pair, one box against two: 16384 x 1024 x 4096 55.5 and 49.5, x 2048
-    // 73.8 and 77.0; 50176 x 2048 x 256 with a shortcut 28.7 and 27.9.  One CTA, with a
-    // shortcut: 200704 x 128 x 512 86.7 and 80.0, x 512 91.0 and 95.7.
-    a.io = kPair ? (a.k_steps >= (c.r ? 12 : 8) ? 1 : 2) : c.r && a.k_steps == 1 ? 2 : 1;
-    const int epi = ((kIo ? 2 * S::kGroups * a.io * kIoBox : S::kEpiWarps * kPatch) + 1023) & ~1023;
-    const int fixed = 1024 + epi + static_cast<int>(sizeof(Tail));
-    a.stages = std::min({(232448 - fixed) / S::kStage, S::kSfStages, 8});
-    // The plain epilogue's loads need L1: 200000 x 64 x 250 with a shortcut 66.0 us
-    // with all of the shared memory taken by the ring, 61.5 with half of it.
-    if (!kIo && c.r)
-        a.stages = std::min(a.stages, std::max(2, (110 * 1024 - fixed) / S::kStage));
-    const int smem = fixed + a.stages * S::kStage;
+    const Memory mem = memory<S, kIo>(c.r != nullptr, a.k_steps);
+    a.io = mem.io;
+    a.stages = mem.stages;
 
     CUtensorMap tmX, tmW, tmXs, tmWs, tmR, tmO;
     const uint64_t str[1] = {static_cast<uint64_t>(c.K) / 2};
@@ -825,7 +858,7 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
         return X1CB_ERR_CUDA;
     const auto kern = conv_mx4_kernel<T, BN, kPair, kIo>;
     if (!opted[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) !=
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
             cudaSuccess)
             return X1CB_ERR_CUDA;
         opted[dev].store(true, std::memory_order_release);
@@ -836,7 +869,7 @@ int run(const Mx4Call &c, int sms, cudaStream_t s)
                                                    : std::min<long long>(tiles, sms)),
                        1, 1);
     cfg.blockDim = dim3(S::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = mem.bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

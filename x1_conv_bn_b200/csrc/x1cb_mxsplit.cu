@@ -310,7 +310,7 @@ template <typename T, int NB> struct Kernel {
     using S = SplitShape<NB>;
     static constexpr int kSmem =
         1024 + S::kStages * S::kStage + S::kPart + static_cast<int>(sizeof(SplitTail));
-    static_assert(kSmem > 114 * 1024, "two of these kernels would share an SM");
+    static_assert(kSmem >= kSmemAlone, "two of these kernels would share an SM");
 
     static int prepare(Fit &fit)
     {

@@ -18,6 +18,8 @@ constexpr int kRChunks = 4;         // 32-channel chunks per residual stage
 constexpr int kRSlotBytes = kRChunks * kTileRows * 32;  // 16 KB
 constexpr int kTmemCols = 512;
 constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block on sm_100
+// Two blocks of this much never share an SM (228 KB, 1 KB of it taken per block).
+constexpr int kSmemAlone = 114 * 1024;
 
 // Status bits of the device status word.
 constexpr unsigned kDevTimeoutProducer = 1u;
