@@ -228,3 +228,30 @@ def test_binding_refuses_gradients():
         with torch.no_grad(), pytest.raises(ValueError) as e:
             call()
         assert "requires grad" not in str(e.value)
+
+
+def test_marshalling_module_of_another_torch_is_rebuilt(tmp_path, monkeypatch):
+    """The module is out of date where it was built for another torch, whatever
+    its times; the built one says what it was built for."""
+    import shutil
+
+    from x1_conv_bn_b200 import _build
+
+    _build.build()
+    assert _build.binding_up_to_date()
+    assert torch.__version__ in X._compiled().built_for
+    copy = tmp_path / "_x1cb_torch.so"
+    shutil.copy2(_build.BINDING, copy)
+    monkeypatch.setattr(_build, "BINDING", str(copy))
+    assert _build.binding_up_to_date()
+    ran = []
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".1")
+    monkeypatch.setattr(_build.subprocess, "run", lambda cmd, **kw: ran.append(cmd) or _Failed)
+    assert not _build.binding_up_to_date()
+    with pytest.raises(RuntimeError):
+        _build.build_binding()
+    assert ran and any(torch.__version__ in a for a in ran[0])
+
+
+class _Failed:
+    returncode, stdout, stderr = 1, "", ""

@@ -45,12 +45,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _built_for() -> str:
+    """What the marshalling module depends on besides its sources; it holds this text."""
+    import torch
+
+    return f"_x1cb_torch for torch {torch.__version__} and {sys.implementation.cache_tag}"
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    if not all(os.path.getmtime(p) <= t for p in (BINDING_SRC, HEADER)):
+        return False
+    with open(BINDING, "rb") as f:
+        return _built_for().encode() + b"\0" in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     """The marshalling module: g++ against torch's headers and libx1cb.so."""
-    if not force and os.path.exists(BINDING):
-        t = os.path.getmtime(BINDING)
-        if all(os.path.getmtime(p) <= t for p in (BINDING_SRC, HEADER)):
-            return BINDING
+    if not force and binding_up_to_date():
+        return BINDING
     import torch
 
     root = os.path.dirname(torch.__file__)
@@ -59,6 +74,7 @@ def build_binding(force: bool = False) -> str:
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DX1CB_BUILT_FOR="{_built_for()}"',
            f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
            f"-I{cuda}/include", f"-I{sysconfig.get_paths()['include']}", BINDING_SRC, "-o", tmp,
            f"-L{root}/lib", f"-L{HERE}", "-l:libx1cb.so", "-lc10", "-lc10_cuda", "-ltorch_cpu",

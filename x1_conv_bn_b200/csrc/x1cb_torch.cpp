@@ -305,4 +305,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_x1cb_torch", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__x1cb_torch(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__x1cb_torch(void)
+{
+    PyObject *m = PyModule_Create(&module);
+    // (the build looks this text up: another torch or Python needs another module)
+    if (m && PyModule_AddStringConstant(m, "built_for", X1CB_BUILT_FOR) < 0)
+        Py_CLEAR(m);
+    return m;
+}
