@@ -339,8 +339,6 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
                 break;
             tc_fence_after();
             const uint32_t d = tmem + turn.acc * S::kSecond;
-            // BN = 64: the tile's scales are the lower or upper half of a 128-row block
-            const uint32_t half = BN == 64 ? (t.nt & 1) * 2u : 0u;
             for (int k = 0; k < a.k_steps; ++k) {
                 if (!wait(full(s), ph)) {
                     ok = false;
@@ -354,11 +352,11 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
                 const int left = (a.K - k * kStageK + 63) / 64;  // K = 64 steps
                 if (left >= 4) {
                     mma_mx4_stage<kPair, S::kBlocks, 4>(d, ad, bd, idesc_mx4(kM, BN, 0),
-                                                        idesc_mx4(kM, BN, 2), sfa, sfw, half,
+                                                        idesc_mx4(kM, BN, 2), sfa, sfw, 0u,
                                                         smem_desc_scales(sf), k > 0);
                 } else if (left == 2) {
                     mma_mx4_stage<kPair, S::kBlocks, 2>(d, ad, bd, idesc_mx4(kM, BN, 0),
-                                                        idesc_mx4(kM, BN, 2), sfa, sfw, half,
+                                                        idesc_mx4(kM, BN, 2), sfa, sfw, 0u,
                                                         smem_desc_scales(sf), k > 0);
                 } else {
                     for (int j = 0; j < (left + 1) / 2; ++j) {
@@ -371,7 +369,7 @@ __global__ void __launch_bounds__(Shape<BN, kPair>::kThreads, 1)
                     }
                     for (int j = 0; j < left; ++j)
                         mma_mx4<kPair>(d, ad + 2 * j, bd + 2 * j, idesc_mx4(kM, BN, (j & 1) * 2),
-                                       sfa + 4 * (j >> 1), sfw + S::kBlocks * 4 * (j >> 1) + half,
+                                       sfa + 4 * (j >> 1), sfw + S::kBlocks * 4 * (j >> 1),
                                        k > 0 || j > 0);
                 }
                 commit(empty(s));
