@@ -332,6 +332,8 @@ size_t group_norm_workspace_size(int dtype, int B, int H, int W, int C, int G);
  *   y = act((x - mu) / sqrt(var + eps) * gamma[c] + beta[c] + r)
  *   x, r, y [B, H, W, C] of `dtype` (r may be NULL); gamma, beta [C] float
  *   (NULL: 1, 0); G groups, C % G == 0; C <= 8192; eps >= 0.
+ * (Squares of deviations from the mean are 32-bit: from about 1e19 on the
+ * variance is infinite and y is act(beta + r).)
  */
 int group_norm_act(const void *x, int dtype, const float *gamma, const float *beta,
                    const void *r, int act, float eps, void *y, void *workspace,

@@ -367,7 +367,10 @@ long long units_of(const Mx4Call &c, int NB)
 
 // CTAs to split K over.  64 x 4096 x 1792: 10.6 us with one, 10.3 with two, 7.9 with
 // four, 6.9 with eight; 64 x 4096 x 2048, whose 16 clusters of eight do not run at
-// once, 13.0 with eight, 7.9 with four; 64 x 1024 x 512 7.2, 8.6, 7.0, 6.5.
+// once, 13.0 with eight, 7.9 with four; 64 x 1024 x 512 7.2, 8.6, 7.0, 6.5.  Where
+// clusters of four do not run at once either, one against two: 2 x 4096 x 8192 7.7 and
+// 6.5, 16 x 4096 x 4800 7.9 and 6.8, 64 x 4096 x 8192 10.6 and 10.6, 64 x 8192 x 9472 15.5
+// and 13.0, 64 x 16384 x 8192 24.6 and 18.2.
 int split_for(long long units, int k_steps, const Fit &fit)
 {
     return k_steps >= 4 && units <= fit.of8   ? 8

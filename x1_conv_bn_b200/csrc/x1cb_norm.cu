@@ -9,10 +9,11 @@
 // values, n (mean - k)^2 <= (n/m) M2, so the subtraction costs at most a factor 8 of
 // the relative rounding error, however far the data lies from zero or one value from
 // the others (about the first alone, with that one of 64 pixels far off, the results
-// were 8 times their tolerance away).  A block joins its threads' (n, mean, M2) about the mean R of one of
-// them, S1 = sum n (mean - R) and S2 = sum M2 + n (mean - R)^2, and where R lies so
-// far off that S2 - S1^2/n would lose more than four bits, once more about the mean
-// found; parts of different blocks are joined in 64 bits.  All in a fixed order.
+// were 8 times their tolerance away).  A block joins its threads' (n, mean, M2) about
+// the mean R of one of them, S1 = sum n (mean - R) and S2 = sum M2 + n (mean - R)^2,
+// and where R lies so far off that S2 - S1^2/n would lose more than four bits, once
+// more about the mean found; parts of different blocks are joined in 64 bits.  All in
+// a fixed order.
 //
 // Two forms.  Where an image (or a slice of its channels that holds whole
 // groups) fits the shared memory of a cluster of up to eight CTAs, one launch
@@ -23,9 +24,11 @@
 // one between the two that joins the chunks, where there are many).
 //
 // 256 x 28 x 28 x 512 of bfloat16 with a shortcut: 112 us, 5.5 TB/s, bound by memory
-// (without one 74 us, 5.6 TB/s); to int8 (128 images) 41 us and to MX4 92 us, bound by
-// instructions: two CTAs fit an SM, and while they round, nothing loads.  SiLU adds
-// 26 us of exponentials and divisions.  Two launches: 1 x 2048 x 2048 x 256 1130 us, x
+// (without one 74 us, 5.6 TB/s).  To int8 (128 images) 41 us and to MX4 92 us: two CTAs
+// fit an SM and go through their phases much together, so that loading and rounding
+// come one after the other (to MX4 40 us of bytes and 52 us of instructions; memory at
+// 31 % of its peak, the SMs at 57 %).  SiLU adds 28 us of exponentials and divisions.
+// Two launches: 1 x 2048 x 2048 x 256 1130 us, x
 // read twice and y written at 5.7 TB/s.  1 x 7 x 7 x 2048: 3.8 us, latency.
 #include <cuda_runtime.h>
 
