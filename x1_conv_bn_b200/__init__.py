@@ -585,7 +585,7 @@ def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str =
     """Group norm (+ shortcut Sum when r is given) + activation, channels last.
 
     x, r, out [B, H, W, C] float32, bfloat16 or float16; gamma, beta [C]
-    float32 or None; G groups; act "none", "relu" or "silu"."""
+    float32 or None; G groups; act "none", "relu" or "silu".  Forward only."""
     if out is None and workspace is None and stream is None:
         y = (_fast or _compiled()).norm(0, x, gamma, beta, G, eps, r, ACTS.get(act, -1), 0.0)
         if y is not None:
@@ -604,7 +604,7 @@ def group_norm_act(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str =
 def group_norm_act_i8(x, gamma, beta, G: int, q_mul: float, eps: float = 1e-5, r=None,
                       act: str = "relu", out=None, workspace=None, stream=None):
     """group_norm_act quantised for the int8 convolutions: clamp(rint(y * q_mul),
-    -128, 127) as NC/32HW32 [B, C/32, H, W, 32]."""
+    -128, 127) as NC/32HW32 [B, C/32, H, W, 32].  Forward only."""
     if out is None and workspace is None and stream is None:
         y = (_fast or _compiled()).norm(1, x, gamma, beta, G, eps, r, ACTS.get(act, -1), q_mul)
         if y is not None:
@@ -639,7 +639,7 @@ def _mx4_outs(lead, M, K, out, index, stream):
 def group_norm_act_mx4(x, gamma, beta, G: int, eps: float = 1e-5, r=None, act: str = "relu",
                        out=None, workspace=None, stream=None):
     """group_norm_act quantised to MX4: (codes [B, H, W, C/2], scales), the
-    operand of conv1x1_bias_add_act_mx4."""
+    operand of conv1x1_bias_add_act_mx4.  Forward only."""
     if out is None and workspace is None and stream is None:
         y = (_fast or _compiled()).norm(2, x, gamma, beta, G, eps, r, ACTS.get(act, -1), 0.0)
         if y is not None:
@@ -660,7 +660,7 @@ def x1cb_mx4_scale_size(M: int, K: int) -> int:
 def x1cb_quantize_mx4(x, out=None, stream=None):
     """x [..., K] float32, bfloat16 or float16 -> MX4 (codes [..., K/2] uint8,
     scales [ceil(M/128), ceil(K/128), 32, 16] uint8), M the product of the
-    leading sizes; K % 32 == 0."""
+    leading sizes; K % 32 == 0.  Forward only."""
     if out is None and stream is None:
         y = (_fast or _compiled()).quantize(x)
         if y is not None:
@@ -706,7 +706,7 @@ def conv1x1_bias_add_act_mx4(x, xs, w, ws, bias=None, r=None, act: str = "relu",
 
     x [B, H, W, Ic/2], xs MX4 activations; w [Oc, Ic/2], ws MX4 weights; bias
     [Oc] float32 or None; r, out [B, H, W, Oc] of `dtype` (float32, bfloat16 or
-    float16)."""
+    float16).  Forward only."""
     if out is None and stream is None:
         y = (_fast or _compiled()).conv1x1(x, xs, w, ws, bias, r, ACTS.get(act, -1),
                                            DTYPES.get(dtype, -1))
